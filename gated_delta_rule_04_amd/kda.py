@@ -32,6 +32,8 @@ ABI_VERSION = 10
 
 EXPORTED = ["kda_chunk_fwd_workspace_bytes", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_prologue", "kda_recurrent_step_prologue", "kda_chunk_bwd_workspace_bytes", "kda_chunk_bwd", "kda_chunk_fwd_save", "kda_chunk_bwd_saved", "kda_chunk_bwd_prologue_workspace_bytes", "kda_chunk_bwd_prologue", "kda_recurrent_step", "kda_recurrent_step_pool", "kda_recurrent_step_pool_prologue",
             "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_bytes", "kda_short_conv_bwd", "kda_short_conv_step",
+            "kda_mla_cache_append", "kda_mla_paged_workspace_bytes", "kda_mla_paged_attn", "kda_mla_attn_fwd",
+            "kda_mla_attn_bwd_workspace_bytes", "kda_mla_attn_bwd",
             "kda_status_str", "kda_abi_version"]
 
 _lib = None
@@ -53,7 +55,7 @@ def lib():
         raise RuntimeError("libkda.so not found at %s; build it with "
                            "`python -m gated_delta_rule_04_amd.build`" % LIB_PATH)
     L = ctypes.CDLL(LIB_PATH)
-    vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, i, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     L.kda_abi_version.restype = i
     L.kda_abi_version.argtypes = []
     L.kda_status_str.restype = ctypes.c_char_p
@@ -94,6 +96,18 @@ def lib():
     L.kda_short_conv_bwd.argtypes = [vp] * 9 + [i] * 6 + [vp, sz, vp]
     L.kda_short_conv_step.restype = i
     L.kda_short_conv_step.argtypes = [vp, vp, vp, vp, i, i, i, i, vp]
+    L.kda_mla_cache_append.restype = i
+    L.kda_mla_cache_append.argtypes = [vp, vp, f, vp, i, i, vp, vp, vp, i, i, vp, vp, i, i, i, i, i, vp]
+    L.kda_mla_paged_workspace_bytes.restype = sz
+    L.kda_mla_paged_workspace_bytes.argtypes = [i] * 8
+    L.kda_mla_paged_attn.restype = i
+    L.kda_mla_paged_attn.argtypes = [vp] * 7 + [i] * 8 + [f, i, vp, sz, vp]
+    L.kda_mla_attn_fwd.restype = i
+    L.kda_mla_attn_fwd.argtypes = [vp] * 6 + [i] * 7 + [f, i, vp]
+    L.kda_mla_attn_bwd_workspace_bytes.restype = sz
+    L.kda_mla_attn_bwd_workspace_bytes.argtypes = [i] * 8
+    L.kda_mla_attn_bwd.restype = i
+    L.kda_mla_attn_bwd.argtypes = [vp] * 10 + [i] * 7 + [f, i, vp, sz, vp]
     _lib = L
     return L
 

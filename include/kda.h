@@ -403,6 +403,143 @@ kda_status kda_short_conv_bwd(const void* x, const void* weight, const void* con
 kda_status kda_short_conv_step(const void* x, const void* weight, void* conv_state, void* y, int N, int C, int W,
                                kda_dtype dt, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Latent attention: the other mixer of the hybrid models (miniKimiK3 card,
+ * "Architecture": nine KDA layers and four latent-attention layers; the
+ * Kimi-K3-Tiny-L13 card gives the same 3:1 layer schedule).  A token's keys
+ * and values for all heads come from one latent vector c_t of R channels and
+ * one rotary key of Dr channels shared by the heads (Dr = 0: no positional
+ * rotation).  The pages give no formula; the standard reading is built:
+ *
+ *   expanded   k_t,h = [W_k,h c_t ; r_t],  v_t,h = W_v,h c_t
+ *              o_i,h = sum_j p_ij v_j,h,   p_i = softmax_j<=i(scale q_i,h . k_j,h)
+ *   absorbed   q'_i,h = [W_k,h^T q_i,h[:Dn] ; q_i,h[Dn:]],   keys [c_j ; r_j],
+ *              o'_i,h = sum_j p_ij c_j  (the caller applies W_v,h afterwards)
+ *
+ * The projections are plain matrix products of the caller's; the expanded
+ * form trains (forward and backward below), the absorbed form serves from a
+ * paged cache of the rows [c_t ; r_t].  All of it is causal.
+ *
+ * Shared by the five calls: dt is KDA_BF16 (KDA_F32 and KDA_F16 return
+ * KDA_ERR_UNSUPPORTED); scores, softmax statistics, sums and log-sum-exps
+ * are float32, results are rounded once at the end; 1 <= H <= 1024; every
+ * bf16 and float tensor 16-byte aligned, a workspace 256-byte aligned
+ * (KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE).  scale must be finite and
+ * positive (KDA_ERR_SHAPE).  A non-finite value may reach every row of its
+ * own sequence, never another sequence's.
+ * ------------------------------------------------------------------------- */
+
+/* Prepares new tokens for the absorbed form: their cache rows, normalised and
+ * rotated, are written into a paged cache, and the queries' rotary parts are
+ * rotated into place.  For token t with position p = positions[t]:
+ *
+ *   row[0:R]    = c[t][0:R] * norm_weight / sqrt(mean(c[t][0:R]^2) + eps)
+ *                 (c[t][0:R] as it is when norm_weight is NULL)
+ *   row[R:R+Dr] = rot(c[t][R:R+Dr], p)
+ *   cache row slots[t] = row;   q[t][h][R:R+Dr] = rot(q_pe[t][h], p)
+ *   rot(x, p): pairs (x_a, x_b) -> (x_a cos - x_b sin, x_b cos + x_a sin) with
+ *   cos = rope[p][i], sin = rope[p][Dr/2 + i]; pair i is channels (i, i + Dr/2),
+ *   or (2i, 2i+1) when interleaved is nonzero.  rope NULL: rot(x, p) = x.
+ *
+ *   c_kv   [T, R + Dr] dt     the down-projection's rows
+ *   norm_weight  [R] f32 or NULL;   eps >= 0
+ *   rope   [num_pos, Dr] f32 or NULL; a position outside [0, num_pos) is
+ *          clamped into it, so that no access leaves the table
+ *   positions  device int32 [T] (may be NULL without rope)
+ *   slots  device int32 [T]: page * page_size + offset of the token's cache
+ *          row.  A value outside [0, num_pages * page_size) marks a token
+ *          that is not kept (padding): no cache row is written for it.  Two
+ *          tokens must not name the same slot (their writes would race).
+ *   cache  [num_pages, page_size, R + Dr] dt, updated in place: the rows
+ *          named by slots only
+ *   q_pe   [T, H, Dr] dt or NULL: with it, q [T, H, R + Dr] dt gets the
+ *          rotated rows in its last Dr channels (for every token, kept or
+ *          not); its other channels are not touched.  H is read only then.
+ * Supported: R in {128, 256, 512}, Dr in {0, 64}; num_pages * page_size below
+ * 2^31.  T = 0 is a no-op.  Errors: KDA_ERR_NULL (also a rope without
+ * positions, q_pe without q), KDA_ERR_SHAPE (also eps < 0 or NaN, rope with
+ * num_pos < 1), KDA_ERR_DTYPE, KDA_ERR_UNSUPPORTED (also q_pe or rope with
+ * Dr = 0), KDA_ERR_HIP.
+ */
+kda_status kda_mla_cache_append(const void* c_kv, const float* norm_weight, float eps, const float* rope,
+                                int num_pos, int interleaved, const int* positions, const int* slots, void* cache,
+                                int num_pages, int page_size, const void* q_pe, void* q, int T, int H, int R, int Dr,
+                                kda_dtype dt, void* stream);
+
+/* Bytes of device workspace kda_mla_paged_attn needs for these sizes (the
+ * partial results of the work split over a long cache); 0 for invalid sizes. */
+size_t kda_mla_paged_workspace_bytes(int N, int Tq, int H, int R, int Dr, int page_size, int max_pages,
+                                     kda_dtype dt);
+
+/* Absorbed latent attention of new tokens over a paged cache: single tokens
+ * (decode) or a chunk of new tokens a sequence (chunked prefill).  Sequence n
+ * has L = seq_lens[n] rows in the cache, its new tokens the last ones; with
+ * Lq new tokens, new token i sees the cache rows j <= L - Lq + i, j >= 0.
+ *
+ *   q      [Tq, H, R + Dr] dt  absorbed queries, sequence after sequence
+ *   cache  [num_pages, page_size, R + Dr] dt
+ *   block_table  device int32 [N, max_pages]: row j of sequence n is row
+ *          j % page_size of page block_table[n][j / page_size].  The rows of
+ *          a page outside [0, num_pages) are left out, as masked ones.
+ *   seq_lens  device int32 [N]; clamped into [0, max_pages * page_size]
+ *   cu_seqlens  device int32 [N + 1] or NULL.  NULL: one new token a
+ *          sequence, Tq = N.  Else sequence n's new tokens are rows
+ *          cu[n] .. cu[n+1]-1 of q (none is fine).  The caller guarantees
+ *          cu[0] = 0, non-decreasing, cu[N] <= Tq; values are clamped into
+ *          [0, Tq].  Rows of q from cu[N] on are padding: their rows of o and
+ *          lse are left as they were.
+ *   o      [Tq, H, R] dt;   lse [Tq, H] f32 or NULL: log(sum_j exp(scale q.k_j)).
+ *          A row that sees nothing gives o = 0 and lse = -infinity.
+ *   workspace  at least kda_mla_paged_workspace_bytes(...) bytes; scratch.
+ * Cache rows past seq_lens[n] may hold anything, NaN too.  Supported: R in
+ * {128, 256, 512}, Dr in {0, 64}, page_size >= 1; num_pages * page_size,
+ * max_pages * page_size and Tq * H below 2^31, N at most 65536.  N = 0 or
+ * Tq = 0 is a no-op.  Errors as elsewhere.
+ */
+kda_status kda_mla_paged_attn(const void* q, const void* cache, const int* block_table, const int* seq_lens,
+                              const int* cu_seqlens, void* o, float* lse, int N, int Tq, int H, int R, int Dr,
+                              int num_pages, int page_size, int max_pages, float scale, kda_dtype dt,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Expanded latent attention, causal, over dense batches or packed documents.
+ *
+ *   q      [B, T, H, Dn + Dr] dt
+ *   kv     [B, T, H, Dn + Dv] dt  each head's key part and value, the
+ *          up-projection's rows
+ *   k_pe   [B, T, Dr] dt  the rotary key shared by the heads (ignored, may be
+ *          NULL, when Dr = 0).  q's last Dr channels and k_pe come rotated.
+ *   o      [B, T, H, Dv] dt;   lse [B, T, H] f32 or NULL (kept for the backward)
+ *   cu_seqlens, num_seqs, B, T: as for kda_chunk_fwd, but cu[N] may be below
+ *          T: tokens from cu[N] on are padding, their outputs left as they were.
+ * Supported: Dn = Dv in {64, 128}, Dr in {0, 64}.  Errors as for
+ * kda_chunk_fwd; no workspace.
+ */
+kda_status kda_mla_attn_fwd(const void* q, const void* kv, const void* k_pe, void* o, float* lse,
+                            const int* cu_seqlens, int num_seqs, int B, int T, int H, int Dn, int Dr, int Dv,
+                            float scale, kda_dtype dt, void* stream);
+
+/* Bytes of device workspace kda_mla_attn_bwd needs: each row's <dout, o>, and
+ * each head's share of the shared rotary key's gradient (float32).  0 for
+ * invalid sizes. */
+size_t kda_mla_attn_bwd_workspace_bytes(int B, int T, int H, int Dn, int Dr, int Dv, int num_seqs, kda_dtype dt);
+
+/* Backward of kda_mla_attn_fwd: the gradients of L = <dout, o>.
+ *
+ *   q, kv, k_pe, cu_seqlens, num_seqs, sizes, scale: the forward's
+ *   o, lse  the forward's outputs
+ *   dout   [B, T, H, Dv] dt
+ *   dq [B, T, H, Dn + Dr] dt;  dkv [B, T, H, Dn + Dv] dt;
+ *   dk_pe  [B, T, Dr] dt: summed over the heads (ignored when Dr = 0)
+ *   workspace  at least kda_mla_attn_bwd_workspace_bytes(...) bytes; scratch.
+ * Tokens from cu[N] on are padding: their gradients are left as they were.
+ * Gradients of different documents never mix.  No atomics: bitwise
+ * deterministic.  Errors as for kda_chunk_bwd.
+ */
+kda_status kda_mla_attn_bwd(const void* q, const void* kv, const void* k_pe, const void* o, const float* lse,
+                            const void* dout, void* dq, void* dkv, void* dk_pe, const int* cu_seqlens,
+                            int num_seqs, int B, int T, int H, int Dn, int Dr, int Dv, float scale, kda_dtype dt,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* kda_status_str(kda_status s);
 
