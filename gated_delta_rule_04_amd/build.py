@@ -40,6 +40,10 @@ COMMON = [
 SOURCE_FLAGS = {
     "kda_prefill_pipe.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"],
     "kda_decode.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"],
+    # 256 of the paged attention's 512 registers are one product's sums: matrix
+    # instructions selected with vector-register results leave the allocator
+    # free to put them in either half (600 spilled registers without it).
+    "mla_paged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

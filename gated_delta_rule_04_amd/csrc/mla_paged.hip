@@ -1,73 +1,471 @@
-// Absorbed latent attention over the paged cache: a wavefront a query row,
-// 64 cache rows at a time with the running maximum and sum of the softmax.
+// Absorbed latent attention over the paged cache.
+//
+// The rows of a sequence's queries (new token, head) are cut into blocks of 32
+// WQ, the cache into tiles of 64 rows; a unit of work is a block and a tile.
+// Each workgroup takes an equal, contiguous run of all units, so a long cache
+// is split over as many workgroups as there are, whatever the lengths; a block
+// that ends up split leaves float32 partial results (sums, running maximum and
+// row sum) that combine_kernel joins.  The split depends on the sizes and
+// lengths alone, and the parts are joined in order.
+//
+// A wavefront owns 32 query rows: S^T = C Q^T with the queries as B operands
+// in registers, the softmax a row a lane, O^T += C^T P^T with all R channels
+// of O^T in accumulators (256 registers at R = 512), so wavefronts share
+// nothing but the tile.  With few rows two wavefronts take the two halves of
+// each tile for the same rows and are joined at the end of a run.
+// Tiles come from the pages straight into LDS (no registers pass through),
+// the next one on its way during a tile, 16-byte pieces permuted within a row
+// so that both the row reads and the transposing reads spread over the banks.
 
+#include <limits.h>
 #include <math.h>
 
-#include "mla_simple.h"
+#include "mla_tile.h"
 
 namespace mla {
 namespace {
 
-template <int R, int DR>
-__global__ __launch_bounds__(64) void paged_kernel(PagedArgs a) {
-  constexpr int D = R + DR;
-  const int i = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-  // sequence of query row i: the last n with cu[n] <= i
-  int n = i, first = i, last = i + 1;
+constexpr int kTile = 64;  // cache rows of a tile
+
+// How a call is cut; the host and the kernels agree on it.
+struct PagedPlan {
+  int wq;             // wavefronts of 32 rows in a block
+  int groups;         // workgroups
+  size_t ml, o, total;  // workspace: unit prefix of the sequences at 0, (maximum, sum) rows, partial sums
+};
+
+// Block height by the rows a sequence has: 32 rows keep 1 wavefront pair busy,
+// 128 rows read each tile once for all heads of up to 128.  Workgroups: as many
+// as run at once (LDS: one a CU at R = 512 and 256, two at 128), or the units
+// there can be.
+PagedPlan paged_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
+  PagedPlan p;
+  const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
+  p.wq = per <= 32 ? 1 : per <= 64 ? 2 : 4;
+  const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
+  const long long most = R == 128 ? 512 : 256, units = blocks * (tiles > 0 ? tiles : 1);
+  p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
+  const size_t slots = 2 * (size_t)p.groups * 32 * p.wq;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.ml = up(((size_t)N + 1) * sizeof(long long));
+  p.o = p.ml + up(slots * 2 * sizeof(float));
+  p.total = p.o + slots * R * sizeof(float);
+  return p;
+}
+
+struct PagedWork {
+  PagedArgs a;
+  long long* prefix;  // [N + 1]: units before sequence n
+  float* ml;          // [2 * groups][block rows][2]
+  float* po;          // [2 * groups][block rows][R]
+};
+
+// A sequence's share: its rows of q, its cache length and its units.
+struct Sequence {
+  int first, Lq, L, blocks, tiles;
+  __device__ __forceinline__ long long units() const { return (long long)blocks * tiles; }
+};
+template <int ROWS>
+__device__ __forceinline__ Sequence sequence(const PagedArgs& a, int n) {
+  Sequence s;
+  int last = n + 1;
+  s.first = n;
+  if (a.cu) document(a.cu, a.Tq, n, s.first, last);
+  s.Lq = last - s.first;
+  s.L = min(max(a.lens[n], 0), a.max_pages * a.page_size);
+  s.blocks = (s.Lq * a.H + ROWS - 1) / ROWS;
+  s.tiles = max((s.L + kTile - 1) / kTile, 1);
+  return s;
+}
+
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// 16 bytes a lane from global memory to lds + 16 lane (M0 holds the base; it
+// may not be read in the cycle after it is written).  Not seen by the
+// compiler's wait counts: tile_barrier waits for it.
+__device__ __forceinline__ void load_lds(const bf16* from, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from)
+               : "memory", "m0");
+}
+
+template <int R, int DR, int WQ>
+struct Paged {
+  static constexpr int D = R + DR, WK = WQ == 4 ? 1 : 2, kWaves = WQ * WK, kThreads = 64 * kWaves;
+  static constexpr int kRows = 32 * WQ;
+  static constexpr int kSub = 2 / WK;  // 32-row halves of a tile a wavefront takes
+};
+
+template <int R, int DR, int WQ>
+__global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(PagedWork w) {
+  using C = Paged<R, DR, WQ>;
+  constexpr int D = C::D;
+  __shared__ __align__(1024) bf16 lat[2][kTile * R];
+  __shared__ __align__(1024) bf16 rot[2][DR ? kTile * DR : 8];
+  __shared__ long long scan[C::kWaves + 1];
+  __shared__ long long found[2];
+  __shared__ float edge[2][C::kRows];
+  const PagedArgs& a = w.a;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wk = wave / WQ;
+
+  // ---- this workgroup's run of units ----
+  // Inclusive sum over the workgroup of one value a thread; the total in scan[kWaves].
+  auto block_scan = [&](long long x) {
+    for (int m = 1; m < 64; m <<= 1) {
+      const long long y = __shfl_up(x, m);
+      if (lane >= m) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) scan[wave] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int i = 0; i < C::kWaves; ++i) {
+      if (i < wave) before += scan[i];
+      all += scan[i];
+    }
+    __syncthreads();
+    if (tid == 0) scan[C::kWaves] = all;
+    __syncthreads();
+    return x + before;
+  };
+  long long total = 0;
+  for (int n0 = 0; n0 < a.N; n0 += C::kThreads) {
+    const int n = n0 + tid;
+    const long long mine = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
+    const long long incl = block_scan(mine) + total;
+    if (blockIdx.x == 0 && n < a.N) w.prefix[n] = incl - mine;
+    total += scan[C::kWaves];
+  }
+  if (blockIdx.x == 0 && tid == 0) w.prefix[a.N] = total;
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long begin = share * blockIdx.x, end = min(begin + share, total);
+  if (begin >= end) return;
+  {
+    long long before = 0;
+    for (int n0 = 0; n0 < a.N; n0 += C::kThreads) {
+      const int n = n0 + tid;
+      const long long mine = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
+      const long long incl = block_scan(mine) + before;
+      if (incl - mine <= begin && begin < incl) {
+        found[0] = n;
+        found[1] = incl - mine;
+      }
+      before += scan[C::kWaves];
+      if (begin < before) break;
+    }
+    __syncthreads();
+  }
+  int n = (int)found[0];
+  long long base = found[1];  // units before sequence n
+  Sequence sq = sequence<C::kRows>(a, n);
+  const float c = a.scale * kda::kLog2e;
+  const unsigned lds_lat = (unsigned)(size_t)(__attribute__((address_space(3))) char*)&lat[0][0];
+  const unsigned lds_rot = (unsigned)(size_t)(__attribute__((address_space(3))) char*)&rot[0][0];
+
+  // LDS addresses of this lane's fragments: row l32 of the latents and of the rotary keys, and the transposing
+  // read's row and column (tr_frag's places)
+  const int te = 4 * half + ((lane >> 2) & 3);
+  const unsigned at_k = l32 * (R * 2) + 32 * (lane & 7) + 16 * half;
+  const unsigned at_r = l32 * (DR * 2) + 32 * ((lane >> 1) & 3) + 16 * half;
+  const unsigned at_t = te * (R * 2) + ((((lane >> 4) & 1) ^ te) * 32) + ((lane >> 1) & 1) * 16 + (lane & 1) * 8;
+
+  for (long long u = begin; u < end;) {
+    while (u >= base + sq.units()) {
+      base += sq.units();
+      sq = sequence<C::kRows>(a, ++n);
+    }
+    const int block = (int)((u - base) / sq.tiles), t0 = (int)((u - base) % sq.tiles);
+    const int t1 = (int)min((long long)sq.tiles, t0 + (end - u));
+    const bool whole = t0 == 0 && t1 == sq.tiles;
+    const int slot = 2 * blockIdx.x + (u == begin ? 0 : 1);
+    u += t1 - t0;
+    const int rows = sq.Lq * a.H;
+    // the last cache row that a row of the block, and this lane's row, sees
+    const int seen = sq.L - sq.Lq + (min(rows, (block + 1) * C::kRows) - 1) / a.H;
+    const int stop = min(t1, seen < 0 ? 0 : seen / kTile + 1);
+    const int m0 = block * C::kRows + 32 * wq, mi = m0 + l32;
+    const bool on = mi < rows;
+    const int lim = on ? sq.L - sq.Lq + mi / a.H : INT_MAX;  // a row that is not one: zero queries, not written
+    const long long row = (long long)sq.first * a.H + mi;
+    const int* table = a.table + (long long)n * a.max_pages;
+
+    // place of the lane's cache row of tile t, -1 when it is not there
+    auto place = [&](int t) {
+      const unsigned j = (unsigned)t * kTile + lane, p = j / (unsigned)a.page_size;
+      int r = -1;
+      if (j < (unsigned)sq.L) {
+        const int page = table[p];
+        if ((unsigned)page < (unsigned)a.num_pages) r = (int)((unsigned)page * a.page_size + (j - p * a.page_size));
+      }
+      return r;
+    };
+    // tile into buffer b; rows that are not there read row 0 of the cache and are cleared later
+    auto fetch = [&](int place, int b) {
+      const int from = max(place, 0);
+      constexpr int kPer = 512 / R;  // rows of one 1024-byte load
+#pragma unroll
+      for (int i = 0; i < kTile / kPer / C::kWaves; ++i) {
+        const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
+        const int at = R == 512 ? __builtin_amdgcn_readlane(from, r0) : __shfl(from, r);
+        const int piece = (lane % (R / 8)) ^ (2 * (r & 7));
+        load_lds(a.cache + (long long)at * D + piece * 8, lds_lat + (b * kTile + r0) * (R * 2));
+      }
+      if constexpr (DR > 0) {
+#pragma unroll
+        for (int i = 0; i < 8 / C::kWaves; ++i) {
+          const int r0 = (wave + C::kWaves * i) * 8, r = r0 + lane / 8;
+          const int at = __shfl(from, r);
+          const int piece = (lane % 8) ^ (2 * ((r >> 1) & 3));
+          load_lds(a.cache + (long long)at * D + R + piece * 8, lds_rot + (b * kTile + r0) * (DR * 2));
+        }
+      }
+    };
+
+    f32x16 acc[R / 32] = {};
+    float m = -FLT_MAX, l = 0.f;
+    if (t0 < stop) {
+      int here = place(t0), next = t0 + 1 < stop ? place(t0 + 1) : -1;
+      __syncthreads();  // the run before is done with the buffers
+      fetch(here, 0);
+      bf16x8 qf[D / 16];
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) qf[s] = on ? row_frag(a.q + row * D, s, half) : bf16x8{};
+      for (int t = t0; t < stop; ++t) {
+        const int b = (t - t0) & 1;
+        tile_barrier();  // tile t is there, and all are done with t - 1
+        const unsigned long long there = __ballot(here >= 0);
+        if (t + 1 < stop) fetch(next, b ^ 1);
+        here = next;
+        if (t + 2 < stop) next = place(t + 2);
+        if (there != ~0ull) {  // uniform: every wavefront has the same 64 places
+          for (int e = tid; e < kTile * (D / 8); e += C::kThreads) {
+            const int r = e / (D / 8), piece = e % (D / 8);
+            if (!((there >> r) & 1))
+              *(u32x4*)(piece < R / 8 ? &lat[b][r * R + piece * 8] : &rot[b][r * DR + (piece - R / 8) * 8]) = u32x4{};
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        if (m0 >= rows) continue;
+        const long long span = (long long)lim - (long long)t * kTile;  // the lane's row sees tile rows 0 .. span
+        unsigned long long sees = there & (span < 0 ? 0ull : span >= 63 ? ~0ull : (2ull << span) - 1);
+        const bool full = __all(sees == ~0ull);
+        sees >>= 4 * half;
+#pragma unroll
+        for (int z = 0; z < C::kSub; ++z) {
+          const int sub = C::kSub == 2 ? z : wk;
+          // Rows are 256 bytes or a multiple: piece 2k of a row, permuted, is at the lane's address with bits
+          // XORed, so 8 addresses serve all k.
+          f32x16 s = {};
+#pragma unroll
+          for (int k = 0; k < R / 16; ++k)
+            s = mma(*(const lds_bf16x8*)(((lds_lat + (b * kTile + 32 * sub) * (R * 2) + at_k) ^ (32 * (k % 8))) + 256 * (k / 8)),
+                    qf[k], s);
+#pragma unroll
+          for (int k = 0; k < DR / 16; ++k)
+            s = mma(*(const lds_bf16x8*)((lds_rot + (b * kTile + 32 * sub) * (DR * 2) + at_r) ^ (32 * k)), qf[R / 16 + k],
+                    s);
+          if (!full) {
+            const unsigned bits = (unsigned)(sees >> (32 * sub));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!((bits >> acc_row(i, 0)) & 1)) s[i] = -INFINITY;
+          }
+          float mx = s[0];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+          mx = halves_max(mx) * c;
+          if (__any(mx > m + 8.f)) {  // as in the expanded forward: a rise below 2^8 keeps the reference
+            const float mn = fmaxf(m, mx), f = kda::fast_exp2(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < R / 32; ++d) acc[d] *= f;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s[i] = kda::fast_exp2(__builtin_fmaf(s[i], c, -m));
+            l += s[i];
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bf16x8 pf = acc_frag(s, k);
+#pragma unroll
+            for (int d = 0; d < R / 32; ++d) {
+              const unsigned at = ((lds_lat + (b * kTile + 32 * sub) * (R * 2) + at_t) ^ (64 * (d % 4))) + 256 * (d / 4) +
+                                  16 * k * (R * 2);
+              const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+              const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * R * 2));
+              acc[d] = mma(__builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), pf, acc[d]);
+            }
+          }
+        }
+      }
+    }
+    l = halves_sum(l);
+    if constexpr (C::WK == 2) {  // the second wavefront of the rows hands over its sums
+      float* hand = reinterpret_cast<float*>(&lat[0][0]) + wq * (32 * R);
+      __syncthreads();
+      if (wk == 1) {
+#pragma unroll
+        for (int d = 0; d < R / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) hand[(16 * d + i) * 64 + lane] = acc[d][i];
+        if (half == 0) {
+          edge[0][32 * wq + l32] = m;
+          edge[1][32 * wq + l32] = l;
+        }
+      }
+      __syncthreads();
+      if (wk == 0) {
+        const float mo = edge[0][32 * wq + l32], mn = fmaxf(m, mo);
+        const float f = kda::fast_exp2(m - mn), g = kda::fast_exp2(mo - mn);
+        l = l * f + edge[1][32 * wq + l32] * g;
+        m = mn;
+#pragma unroll
+        for (int d = 0; d < R / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[d][i] = acc[d][i] * f + hand[(16 * d + i) * 64 + lane] * g;
+      }
+    }
+    if (wk == 0 && on) {
+      if (whole) {
+        const float r = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees nothing
+#pragma unroll
+        for (int d = 0; d < R / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *(u32x2*)(a.o + row * R + 32 * d + acc_row(i, half)) = u32x2{
+                kda::pk_bf16(acc[d][i] * r, acc[d][i + 1] * r), kda::pk_bf16(acc[d][i + 2] * r, acc[d][i + 3] * r)};
+        if (a.lse && half == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kda::kLog2e);
+      } else {
+        const long long at = (long long)slot * C::kRows + 32 * wq + l32;
+#pragma unroll
+        for (int d = 0; d < R / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *(f32x4*)(w.po + at * R + 32 * d + acc_row(i, half)) =
+                f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]};
+        if (half == 0) {
+          w.ml[2 * at] = m;
+          w.ml[2 * at + 1] = l;
+        }
+      }
+    }
+  }
+}
+
+// Joins the parts of split blocks.  A row's R channels are taken by R / SLICE
+// workgroups with SLICE / 4 threads a part: a wavefront-sized slice for few
+// parts a row (4 rows a workgroup), a 128-channel slice with 8 parts at a time
+// for many.
+template <int R, int ROWS, bool MANY>
+__global__ __launch_bounds__(256) void combine_kernel(PagedWork w, int groups) {
+  constexpr int kSlice = MANY ? 128 : R, kAcross = kSlice / 4;      // threads over the channels
+  constexpr int kLanes = MANY ? 256 : 64, kWays = MANY ? kLanes / kAcross : 1;  // threads of a row, parts at a time
+  constexpr int kQuads = MANY ? 1 : R / 256 > 0 ? R / 256 : 1;      // 4-channel pieces a thread (few parts)
+  const PagedArgs& a = w.a;
+  const int tid = threadIdx.x;
+  const long long row = MANY ? blockIdx.x / (R / 128) : (long long)blockIdx.x * 4 + (tid >> 6);
+  if (row >= (long long)a.Tq * a.H) return;
+  int n = (int)(row / a.H);
   if (a.cu) {
     int lo = 0, hi = a.N;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.cu[mid] <= i) lo = mid; else hi = mid;
+    const int token = n;
+    while (hi - lo > 1) {  // the last sequence that starts at or before the token
+      const int step = (hi - lo + 63) / 64, i = lo + (tid & 63) * step;
+      const int count = __popcll(__ballot(i < hi && min(max(a.cu[i], 0), a.Tq) <= token));
+      lo += max(count - 1, 0) * step;
+      hi = min(lo + step, hi);
     }
     n = lo;
-    document(a.cu, a.Tq, n, first, last);
-    if (i < first || i >= last) return;
   }
-  const int L = min(max(a.lens[n], 0), a.max_pages * a.page_size);
-  const int end = min(L, L - (last - i) + 1);
-  const long long row = (long long)i * a.H + h;
-  const bf16* q = a.q + row * D;
-  __shared__ float p[64];
-  __shared__ const bf16* rows[64];
-  float m = -INFINITY, l = 0.f, acc[R / 64] = {};
-  for (int j0 = 0; j0 < end; j0 += 64) {
-    const int j = j0 + lane;
-    const bf16* k = nullptr;
-    if (j < end) {
-      const int page = a.table[(long long)n * a.max_pages + j / a.page_size];
-      if ((unsigned)page < (unsigned)a.num_pages)
-        k = a.cache + ((long long)page * a.page_size + j % a.page_size) * D;
-    }
-    const float s = k ? dot(q, k, D) * a.scale : -INFINITY;
-    const float mx = fmaxf(m, wave_max(s));
-    const float at = mx == -INFINITY ? 0.f : mx;  // nothing but masked rows (or NaN, which the maximum passes over)
-    const float c = expf(m - at), e = k ? expf(s - at) : 0.f;
-    m = mx;
-    l = l * c + wave_sum(e);
-    __syncthreads();
-    p[lane] = e;
-    rows[lane] = k;
-    __syncthreads();
-    for (int d = 0; d < R / 64; ++d) acc[d] *= c;
-    for (int t = 0; t < 64; ++t) {
-      if (!rows[t]) continue;
-      for (int d = 0; d < R / 64; ++d) acc[d] += p[t] * (float)rows[t][d * 64 + lane];
+  const Sequence s = sequence<ROWS>(a, n);
+  const long long in = row - (long long)s.first * a.H;
+  if (in < 0 || in >= (long long)s.Lq * a.H) return;
+  const long long share = (w.prefix[a.N] + groups - 1) / groups;
+  const long long u0 = w.prefix[n] + in / ROWS * s.tiles, u1 = u0 + s.tiles - 1;
+  const int g0 = (int)(u0 / share), g1 = (int)(u1 / share);
+  if (g0 == g1) return;  // in one piece: written already
+  // part g's slot: its run's first segment, unless the block starts inside the run
+  auto place = [&](int g) { return (long long)(2 * g + (g == g0 && u0 != g0 * share ? 1 : 0)) * ROWS + in % ROWS; };
+  float m = -FLT_MAX;
+  for (int g = g0; g <= g1; ++g) m = fmaxf(m, w.ml[2 * place(g)]);
+  float l = 0.f;
+  f32x4 o[kQuads] = {};
+  const int way = MANY ? tid / kAcross : 0;
+  const int ch = MANY ? (blockIdx.x % (R / 128)) * 128 + (tid % kAcross) * 4 : (tid & 63) * 4;
+  const bool in_row = MANY || ch < R;
+#pragma unroll 4
+  for (int g = g0 + way; g <= g1; g += kWays) {
+    const long long at = place(g);
+    const float f = kda::fast_exp2(w.ml[2 * at] - m);
+    l += w.ml[2 * at + 1] * f;
+    if (in_row) {
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) o[q] += *(const f32x4*)(w.po + at * R + ch + 256 * q) * f;
     }
   }
-  for (int d = 0; d < R / 64; ++d) a.o[row * R + d * 64 + lane] = (bf16)(l > 0.f || l != l ? acc[d] / l : 0.f);
-  if (a.lse && lane == 0) a.lse[row] = l > 0.f || l != l ? (m == -INFINITY ? 0.f : m) + logf(l) : -INFINITY;
+  if constexpr (MANY) {
+    __shared__ f32x4 part[kWays][kAcross];
+    __shared__ float lpart[kWays];
+    part[way][tid % kAcross] = o[0];
+    if (tid % kAcross == 0) lpart[way] = l;
+    __syncthreads();
+    if (way != 0) return;
+    for (int i = 1; i < kWays; ++i) {
+      o[0] += part[i][tid];
+      l += lpart[i];
+    }
+  }
+  const float r = l == 0.f ? 0.f : 1.f / l;
+  if (in_row) {
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+      *(u32x2*)(a.o + row * R + ch + 256 * q) =
+          u32x2{kda::pk_bf16(o[q][0] * r, o[q][1] * r), kda::pk_bf16(o[q][2] * r, o[q][3] * r)};
+  }
+  if (a.lse && ch == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kda::kLog2e);
+}
+
+template <int R, int DR, int WQ>
+hipError_t launch(const PagedWork& w, const PagedPlan& p, hipStream_t stream) {
+  using C = Paged<R, DR, WQ>;
+  paged_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w);
+  if (p.groups > 1) {
+    const long long rows = (long long)w.a.Tq * w.a.H;
+    // parts a block can have: with more than 16 a row takes several workgroups
+    if (p.groups > 16 * (rows / C::kRows + 1))
+      combine_kernel<R, C::kRows, true><<<dim3((unsigned)(rows * (R / 128))), dim3(256), 0, stream>>>(w, p.groups);
+    else
+      combine_kernel<R, C::kRows, false><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(w, p.groups);
+  }
+  return hipGetLastError();
 }
 
 template <int R, int DR>
 hipError_t launch(const PagedArgs& a, hipStream_t stream) {
-  paged_kernel<R, DR><<<dim3(a.Tq, a.H), dim3(64), 0, stream>>>(a);
-  return hipGetLastError();
+  const PagedPlan p = paged_plan(a.N, a.Tq, a.H, R, DR, (long long)a.max_pages * a.page_size);
+  char* ws = static_cast<char*>(a.ws);
+  PagedWork w{a, reinterpret_cast<long long*>(ws), reinterpret_cast<float*>(ws + p.ml),
+              reinterpret_cast<float*>(ws + p.o)};
+  if (a.num_pages == 0) w.a.max_pages = 0;  // no cache rows at all: every length is 0
+  switch (p.wq) {
+    case 1: return launch<R, DR, 1>(w, p, stream);
+    case 2: return launch<R, DR, 2>(w, p, stream);
+    default: return launch<R, DR, 4>(w, p, stream);
+  }
 }
 
 }  // namespace
 
-size_t paged_workspace(int, int, int, int, int, long long) { return 0; }
+size_t paged_workspace(int N, int Tq, int H, int R, int Dr, long long max_len) {
+  return N == 0 || Tq == 0 ? 0 : paged_plan(N, Tq, H, R, Dr, max_len).total;
+}
 
 hipError_t launch_paged(int R, int Dr, const PagedArgs& a, hipStream_t stream) {
   switch (R + Dr) {
