@@ -208,7 +208,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
     auto fetch = [&](int place, int b) {
       const int from = max(place, 0);
       constexpr int kPer = 512 / R;  // rows of one 1024-byte load
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < kTile / kPer / C::kWaves; ++i) {
         const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
         const int at = R == 512 ? __builtin_amdgcn_readlane(from, r0) : __shfl(from, r);
@@ -255,7 +255,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
         unsigned long long sees = there & (span < 0 ? 0ull : span >= 63 ? ~0ull : (2ull << span) - 1);
         const bool full = __all(sees == ~0ull);
         sees >>= 4 * half;
-#pragma unroll
+#pragma unroll 1
         for (int z = 0; z < C::kSub; ++z) {
           const int sub = C::kSub == 2 ? z : wk;
           // Rows are 256 bytes or a multiple: piece 2k of a row, permuted, is at the lane's address with bits
@@ -394,7 +394,9 @@ __global__ __launch_bounds__(256) void combine_kernel(PagedWork w, int groups) {
   // part g's slot: its run's first segment, unless the block starts inside the run
   auto place = [&](int g) { return (long long)(2 * g + (g == g0 && u0 != g0 * share ? 1 : 0)) * ROWS + in % ROWS; };
   float m = -FLT_MAX;
-  for (int g = g0; g <= g1; ++g) m = fmaxf(m, w.ml[2 * place(g)]);
+  for (int g = g0 + (tid & 63); g <= g1; g += 64) m = fmaxf(m, w.ml[2 * place(g)]);
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
   float l = 0.f;
   f32x4 o[kQuads] = {};
   const int way = MANY ? tid / kAcross : 0;
