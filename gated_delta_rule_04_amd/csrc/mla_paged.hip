@@ -25,7 +25,8 @@
 namespace mla {
 namespace {
 
-constexpr int kTile = 64;  // cache rows of a tile
+constexpr int kTile = 64;    // cache rows of a tile
+constexpr int kPlaces = 16;  // tiles whose rows' places are looked up at a time
 
 // How a call is cut; the host and the kernels agree on it.
 struct PagedPlan {
@@ -78,9 +79,13 @@ __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int n) {
   return s;
 }
 
+// Waits until at most N of this wavefront's vector memory operations are on
+// their way (they end in order), and for the other wavefronts.
+template <int N>
 __device__ __forceinline__ void tile_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -95,9 +100,10 @@ __device__ __forceinline__ void load_lds(const bf16* from, unsigned lds) {
 
 template <int R, int DR, int WQ>
 struct Paged {
-  static constexpr int D = R + DR, WK = WQ == 4 ? 1 : 2, kWaves = WQ * WK, kThreads = 64 * kWaves;
+  static constexpr bool PAIR = WQ < 4;  // two wavefronts for each 32 rows
+  static constexpr int D = R + DR, kWaves = PAIR ? 2 * WQ : WQ, kThreads = 64 * kWaves;
   static constexpr int kRows = 32 * WQ;
-  static constexpr int kSub = 2 / WK;  // 32-row halves of a tile a wavefront takes
+  static constexpr int kOut = PAIR ? R / 64 : R / 32;  // 32-channel tiles of O a wavefront holds
 };
 
 template <int R, int DR, int WQ>
@@ -108,10 +114,12 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   __shared__ __align__(1024) bf16 rot[2][DR ? kTile * DR : 8];
   __shared__ long long scan[C::kWaves + 1];
   __shared__ long long found[2];
-  __shared__ float edge[2][C::kRows];
+  __shared__ int places[kPlaces * kTile];
+  __shared__ __align__(16) u32x4 handed[C::PAIR ? C::kWaves : 1][2][64];  // a pair's weights, as B operands
+  __shared__ float rise[2][C::kRows], sums[2][C::kRows];
   const PagedArgs& a = w.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wk = wave / WQ;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wd = wave / WQ;
 
   // ---- this workgroup's run of units ----
   // Inclusive sum over the workgroup of one value a thread; the total in scan[kWaves].
@@ -172,7 +180,8 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   const int te = 4 * half + ((lane >> 2) & 3);
   const unsigned at_k = l32 * (R * 2) + 32 * (lane & 7) + 16 * half;
   const unsigned at_r = l32 * (DR * 2) + 32 * ((lane >> 1) & 3) + 16 * half;
-  const unsigned at_t = te * (R * 2) + ((((lane >> 4) & 1) ^ te) * 32) + ((lane >> 1) & 1) * 16 + (lane & 1) * 8;
+  const unsigned at_t = (R == 128 ? 0 : wd * R) + te * (R * 2) + (((((lane >> 4) & 1) ^ te) * 32) ^ (R == 128 ? 128 * wd : 0)) +
+                        ((lane >> 1) & 1) * 16 + (lane & 1) * 8;
 
   for (long long u = begin; u < end;) {
     while (u >= base + sq.units()) {
@@ -194,73 +203,88 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
     const long long row = (long long)sq.first * a.H + mi;
     const int* table = a.table + (long long)n * a.max_pages;
 
-    // place of the lane's cache row of tile t, -1 when it is not there
-    auto place = [&](int t) {
-      const unsigned j = (unsigned)t * kTile + lane, p = j / (unsigned)a.page_size;
-      int r = -1;
-      if (j < (unsigned)sq.L) {
-        const int page = table[p];
-        if ((unsigned)page < (unsigned)a.num_pages) r = (int)((unsigned)page * a.page_size + (j - p * a.page_size));
+    // the places of the rows of tiles p0 .. p0 + kPlaces - 1 into LDS: cache row, -1 when it is not there
+    auto look_up = [&](int p0) {
+      for (int e = tid; e < kPlaces * kTile; e += C::kThreads) {
+        const unsigned j = (unsigned)p0 * kTile + e, p = j / (unsigned)a.page_size;
+        int r = -1;
+        if (j < (unsigned)sq.L) {
+          const int page = table[p];
+          if ((unsigned)page < (unsigned)a.num_pages) r = (int)((unsigned)page * a.page_size + (j - p * a.page_size));
+        }
+        places[e] = r;
       }
-      return r;
     };
-    // tile into buffer b; rows that are not there read row 0 of the cache and are cleared later
-    auto fetch = [&](int place, int b) {
-      const int from = max(place, 0);
+    // a tile into buffer b; rows that are not there read row 0 of the cache and are cleared later
+    auto fetch = [&](const int* from, int b) {
       constexpr int kPer = 512 / R;  // rows of one 1024-byte load
 #pragma unroll 4
       for (int i = 0; i < kTile / kPer / C::kWaves; ++i) {
         const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
-        const int at = R == 512 ? __builtin_amdgcn_readlane(from, r0) : __shfl(from, r);
         const int piece = (lane % (R / 8)) ^ (2 * (r & 7));
-        load_lds(a.cache + (long long)at * D + piece * 8, lds_lat + (b * kTile + r0) * (R * 2));
+        load_lds(a.cache + (long long)max(from[r], 0) * D + piece * 8, lds_lat + (b * kTile + r0) * (R * 2));
       }
       if constexpr (DR > 0) {
 #pragma unroll
         for (int i = 0; i < 8 / C::kWaves; ++i) {
           const int r0 = (wave + C::kWaves * i) * 8, r = r0 + lane / 8;
-          const int at = __shfl(from, r);
           const int piece = (lane % 8) ^ (2 * ((r >> 1) & 3));
-          load_lds(a.cache + (long long)at * D + R + piece * 8, lds_rot + (b * kTile + r0) * (DR * 2));
+          load_lds(a.cache + (long long)max(from[r], 0) * D + R + piece * 8, lds_rot + (b * kTile + r0) * (DR * 2));
         }
       }
     };
+    constexpr int kLoads = (kTile * R / 512 + (DR ? 8 : 0)) / C::kWaves;  // a wavefront's share of a tile
 
-    f32x16 acc[R / 32] = {};
+    f32x16 acc[C::kOut] = {};
     float m = -FLT_MAX, l = 0.f;
     if (t0 < stop) {
-      int here = place(t0), next = t0 + 1 < stop ? place(t0 + 1) : -1;
-      __syncthreads();  // the run before is done with the buffers
-      fetch(here, 0);
       bf16x8 qf[D / 16];
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) qf[s] = on ? row_frag(a.q + row * D, s, half) : bf16x8{};
+      int p0 = t0;
+      __syncthreads();  // the run before is done with the buffers
+      look_up(p0);
+      __syncthreads();
+      fetch(places, 0);
+      if (t0 + 1 < stop) fetch(places + kTile, 1);
+      unsigned long long next = __ballot(places[lane] >= 0);
       for (int t = t0; t < stop; ++t) {
         const int b = (t - t0) & 1;
-        tile_barrier();  // tile t is there, and all are done with t - 1
-        const unsigned long long there = __ballot(here >= 0);
-        if (t + 1 < stop) fetch(next, b ^ 1);
-        here = next;
-        if (t + 2 < stop) next = place(t + 2);
+        if (t > t0) {  // the buffer of tile t - 1 is free: tile t + 1 into it
+          lds_barrier();
+          if (t + 1 < stop) {
+            if (t + 1 == p0 + kPlaces) {
+              look_up(p0 = t + 1);
+              lds_barrier();
+            }
+            fetch(places + (t + 1 - p0) * kTile, b ^ 1);
+          }
+        }
+        if (t + 1 < stop)  // tile t is there, tile t + 1 on its way
+          tile_barrier<kLoads>();
+        else
+          tile_barrier<0>();
+        const unsigned long long there = next;
+        if (t + 1 < stop) next = __ballot(places[(t + 1 - p0) * kTile + lane] >= 0);
         if (there != ~0ull) {  // uniform: every wavefront has the same 64 places
           for (int e = tid; e < kTile * (D / 8); e += C::kThreads) {
             const int r = e / (D / 8), piece = e % (D / 8);
             if (!((there >> r) & 1))
               *(u32x4*)(piece < R / 8 ? &lat[b][r * R + piece * 8] : &rot[b][r * DR + (piece - R / 8) * 8]) = u32x4{};
           }
-          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          lds_barrier();
         }
-        if (m0 >= rows) continue;
+        if (!C::PAIR && m0 >= rows) continue;
         const long long span = (long long)lim - (long long)t * kTile;  // the lane's row sees tile rows 0 .. span
         unsigned long long sees = there & (span < 0 ? 0ull : span >= 63 ? ~0ull : (2ull << span) - 1);
         const bool full = __all(sees == ~0ull);
         sees >>= 4 * half;
-#pragma unroll 1
-        for (int z = 0; z < C::kSub; ++z) {
-          const int sub = C::kSub == 2 ? z : wk;
+        // S^T of 32 rows of the tile, scaled to log2 units later; masked rows at -infinity; its maximum a query
+        f32x16 s;
+        auto scores = [&](int sub) {
+          s = f32x16{};
           // Rows are 256 bytes or a multiple: piece 2k of a row, permuted, is at the lane's address with bits
           // XORed, so 8 addresses serve all k.
-          f32x16 s = {};
 #pragma unroll
           for (int k = 0; k < R / 16; ++k)
             s = mma(*(const lds_bf16x8*)(((lds_lat + (b * kTile + 32 * sub) * (R * 2) + at_k) ^ (32 * (k % 8))) + 256 * (k / 8)),
@@ -278,79 +302,103 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
           float mx = s[0];
 #pragma unroll
           for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
-          mx = halves_max(mx) * c;
-          if (__any(mx > m + 8.f)) {  // as in the expanded forward: a rise below 2^8 keeps the reference
-            const float mn = fmaxf(m, mx), f = kda::fast_exp2(m - mn);
-            m = mn;
-            l *= f;
+          return halves_max(mx) * c;
+        };
+        // The sums keep their reference while the maximum rises by less than 2^8, as in the expanded forward.
+        auto refer = [&](float mx) {
+          const float mn = fmaxf(m, mx), f = kda::fast_exp2(m - mn);
+          m = mn;
+          l *= f;
 #pragma unroll
-            for (int d = 0; d < R / 32; ++d) acc[d] *= f;
-          }
+          for (int d = 0; d < C::kOut; ++d) acc[d] *= f;
+        };
+        auto weights = [&](const f32x16& s, bf16x8* pf) {
+          f32x16 p;
+          float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            s[i] = kda::fast_exp2(__builtin_fmaf(s[i], c, -m));
-            l += s[i];
+            p[i] = kda::fast_exp2(__builtin_fmaf(s[i], c, -m));
+            sum += p[i];
           }
+          pf[0] = acc_frag(p, 0);
+          pf[1] = acc_frag(p, 1);
+          return sum;
+        };
+        auto values = [&](int sub, int k, bf16x8 pf) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const bf16x8 pf = acc_frag(s, k);
+          for (int d = 0; d < C::kOut; ++d) {
+            const unsigned at = ((lds_lat + (b * kTile + 32 * sub) * (R * 2) + at_t) ^ (64 * (d % 4))) + 256 * (d / 4) +
+                                16 * k * (R * 2);
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * R * 2));
+            acc[d] = mma(__builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), pf, acc[d]);
+          }
+        };
+        bf16x8 pf[2];
+        if constexpr (C::PAIR) {
+          // The weights are handed over as they come with the pair's present reference, and formed again only
+          // where a maximum rose past it: one barrier a tile.
+          const float mx = scores(wd);
+          const bool over = mx > m + 8.f;
+          float sum = weights(s, pf);
+          rise[wd][32 * wq + l32] = over ? mx : -FLT_MAX;
+          handed[wave][0][lane] = __builtin_bit_cast(u32x4, pf[0]);
+          handed[wave][1][lane] = __builtin_bit_cast(u32x4, pf[1]);
+          lds_barrier();
+          const int r = lane % C::kRows;
+          if (__any(fmaxf(rise[0][r], rise[1][r]) > -FLT_MAX)) {  // the same for all wavefronts
+            refer(fmaxf(rise[0][32 * wq + l32], rise[1][32 * wq + l32]));
+            sum = weights(s, pf);
+            handed[wave][0][lane] = __builtin_bit_cast(u32x4, pf[0]);
+            handed[wave][1][lane] = __builtin_bit_cast(u32x4, pf[1]);
+            lds_barrier();
+          }
+          l += sum;
 #pragma unroll
-            for (int d = 0; d < R / 32; ++d) {
-              const unsigned at = ((lds_lat + (b * kTile + 32 * sub) * (R * 2) + at_t) ^ (64 * (d % 4))) + 256 * (d / 4) +
-                                  16 * k * (R * 2);
-              const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-              const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * R * 2));
-              acc[d] = mma(__builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), pf, acc[d]);
-            }
+          for (int k = 0; k < 2; ++k) values(wd, k, pf[k]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            values(wd ^ 1, k, __builtin_bit_cast(bf16x8, handed[wq + WQ * (wd ^ 1)][k][lane]));
+        } else {
+#pragma unroll 1
+          for (int sub = 0; sub < 2; ++sub) {
+            const float mx = scores(sub);
+            if (__any(mx > m + 8.f)) refer(mx);
+            l += weights(s, pf);
+            values(sub, 0, pf[0]);
+            values(sub, 1, pf[1]);
           }
         }
       }
     }
     l = halves_sum(l);
-    if constexpr (C::WK == 2) {  // the second wavefront of the rows hands over its sums
-      float* hand = reinterpret_cast<float*>(&lat[0][0]) + wq * (32 * R);
-      __syncthreads();
-      if (wk == 1) {
-#pragma unroll
-        for (int d = 0; d < R / 32; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) hand[(16 * d + i) * 64 + lane] = acc[d][i];
-        if (half == 0) {
-          edge[0][32 * wq + l32] = m;
-          edge[1][32 * wq + l32] = l;
-        }
-      }
-      __syncthreads();
-      if (wk == 0) {
-        const float mo = edge[0][32 * wq + l32], mn = fmaxf(m, mo);
-        const float f = kda::fast_exp2(m - mn), g = kda::fast_exp2(mo - mn);
-        l = l * f + edge[1][32 * wq + l32] * g;
-        m = mn;
-#pragma unroll
-        for (int d = 0; d < R / 32; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[d][i] = acc[d][i] * f + hand[(16 * d + i) * 64 + lane] * g;
-      }
+    if constexpr (C::PAIR) {
+      lds_barrier();  // the run before has read its sums
+      sums[wd][32 * wq + l32] = l;
+      lds_barrier();
+      l = sums[0][32 * wq + l32] + sums[1][32 * wq + l32];
     }
-    if (wk == 0 && on) {
+    if (on) {
+      const int ch = (C::PAIR ? wd * (R / 2) : 0) + 4 * half;
+      const bool first = half == 0 && wd == 0;
       if (whole) {
         const float r = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees nothing
 #pragma unroll
-        for (int d = 0; d < R / 32; ++d)
+        for (int d = 0; d < C::kOut; ++d)
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            *(u32x2*)(a.o + row * R + 32 * d + acc_row(i, half)) = u32x2{
+            *(u32x2*)(a.o + row * R + ch + 32 * d + acc_row(i, 0)) = u32x2{
                 kda::pk_bf16(acc[d][i] * r, acc[d][i + 1] * r), kda::pk_bf16(acc[d][i + 2] * r, acc[d][i + 3] * r)};
-        if (a.lse && half == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kda::kLog2e);
+        if (a.lse && first) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kda::kLog2e);
       } else {
         const long long at = (long long)slot * C::kRows + 32 * wq + l32;
 #pragma unroll
-        for (int d = 0; d < R / 32; ++d)
+        for (int d = 0; d < C::kOut; ++d)
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            *(f32x4*)(w.po + at * R + 32 * d + acc_row(i, half)) =
+            *(f32x4*)(w.po + at * R + ch + 32 * d + acc_row(i, 0)) =
                 f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]};
-        if (half == 0) {
+        if (first) {
           w.ml[2 * at] = m;
           w.ml[2 * at + 1] = l;
         }
@@ -440,8 +488,8 @@ hipError_t launch(const PagedWork& w, const PagedPlan& p, hipStream_t stream) {
   paged_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w);
   if (p.groups > 1) {
     const long long rows = (long long)w.a.Tq * w.a.H;
-    // parts a block can have: with more than 16 a row takes several workgroups
-    if (p.groups > 16 * (rows / C::kRows + 1))
+    // parts a block can have: with more than 4 a row takes several workgroups
+    if (p.groups > 4 * (rows / C::kRows + 1))
       combine_kernel<R, C::kRows, true><<<dim3((unsigned)(rows * (R / 128))), dim3(256), 0, stream>>>(w, p.groups);
     else
       combine_kernel<R, C::kRows, false><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(w, p.groups);
