@@ -40,10 +40,12 @@ COMMON = [
 SOURCE_FLAGS = {
     "kda_prefill_pipe.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"],
     "kda_decode.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"],
-    # 256 of the paged attention's 512 registers are one product's sums: matrix
-    # instructions selected with vector-register results leave the allocator
-    # free to put them in either half (600 spilled registers without it).
+    # Matrix instructions selected with vector-register results leave the
+    # allocator free to keep long-lived sums in either half of the register
+    # file: without it the paged attention's 256 registers of sums at 512
+    # channels spill (600 registers), and dk, dv take 466 registers, not 321.
     "mla_paged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "mla_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

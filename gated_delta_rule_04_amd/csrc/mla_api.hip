@@ -51,7 +51,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(int B, int T, int H, int Dr) {
   BwdLayout L;
   const size_t rows = (size_t)B * T * H;
-  L.pe_part = align256(rows * sizeof(float));
+  L.pe_part = align256(rows * 2 * sizeof(float));
   L.total = L.pe_part + align256(rows * Dr * sizeof(float));
   return L;
 }

@@ -20,29 +20,6 @@ constexpr int kRows = 128;  // queries (or keys) of a workgroup, 32 a wavefront
 constexpr int kK = 32;      // keys of a tile of the dq kernel
 constexpr int kI = 32;      // queries of a tile of the dk, dv kernel
 
-// A tile of ROWS tokens, LDS row stride P: a strided [token][H][W] tensor's
-// channels, or the shared rotary key's.  Pieces of 16 bytes, kept in registers
-// between load and store so that the next tile is on its way during a tile.
-template <int ROWS, int W, int P>
-struct Tile {
-  static constexpr int kPiece = W / 8, kN = ROWS * kPiece / 256;
-  static_assert(W == 0 || (ROWS * kPiece) % 256 == 0, "pieces");
-  u32x4 r[kN ? kN : 1];
-  __device__ __forceinline__ void load(const bf16* base, int stride, int rows, int tid) {
-#pragma unroll
-    for (int p = 0; p < kN; ++p) {
-      const int row = (p * 256 + tid) / kPiece, c = (p * 256 + tid) % kPiece;
-      r[p] = u32x4{};
-      if (row < rows) r[p] = *(const u32x4*)(base + row * stride + c * 8);
-    }
-  }
-  __device__ __forceinline__ void store(bf16* lds, int tid) const {
-#pragma unroll
-    for (int p = 0; p < kN; ++p)
-      *(u32x4*)(lds + ((p * 256 + tid) / (kPiece ? kPiece : 1)) * P + ((p * 256 + tid) % (kPiece ? kPiece : 1)) * 8) = r[p];
-  }
-};
-
 // dq.  Also writes delta for the other kernel, summed as sum_j p dp in float32
 // (the rounded o would put half a bf16 step of o into every ds).  A workgroup
 // that starts a document takes delta from a pass of its own over its 128 keys
@@ -51,13 +28,14 @@ struct Tile {
 // average down.
 template <int DN, int DR>
 __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
-  constexpr int DQ = DN + DR, KP = DQ + kPad, VP = DN + kPad;
-  __shared__ __align__(16) bf16 ks[kK * KP];
-  __shared__ __align__(16) bf16 vs[kK * VP];
+  constexpr int DQ = DN + DR;
+  constexpr unsigned kKey = kK * DN * 2, kRot = kK * DR * 2;  // bytes of a tile's parts: keys, values, rotary keys
+  __shared__ __align__(1024) char lds[2][2 * kKey + kRot];
   int h, len, q0;
   long long t0;
   if (!tile_place<kRows>(a, map, true, h, t0, len, q0)) return;
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, w0 = q0 + (tid >> 6) * 32;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w0 = q0 + wave * 32;
   const int qi = w0 + (lane & 31);
   const int keys = min(len, q0 + kRows);
   const int ld = a.H * 2 * DN;
@@ -81,33 +59,36 @@ __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
   if (on) lse = a.lse[row] * kda::kLog2e;
   const float c = a.scale * kda::kLog2e;
 
-  Tile<kK, DN, KP> tk;
-  Tile<kK, DN, VP> tv;
-  Tile<kK, DR, KP> tp;
+  const unsigned base = lds_address(&lds[0][0]);
+  const LaneAt<DN> at(lane);
+  const LaneAt<64> at_rot(lane);
+  auto fetch = [&](int j0, int b) {
+    const unsigned to = base + b * (2 * kKey + kRot);
+    const bf16* from = kv + (long long)j0 * ld;
+    fetch_rows<kK, DN>(from, ld, len - 1 - j0, to, wave, lane);
+    fetch_rows<kK, DN>(from + DN, ld, len - 1 - j0, to + kKey, wave, lane);
+    if constexpr (DR > 0) fetch_rows<kK, DR>(pe + (long long)j0 * DR, DR, len - 1 - j0, to + 2 * kKey, wave, lane);
+  };
   f32x16 acc[DQ / 32] = {};
   float sum = 0.f;  // this lane's half of sum_j p dp
   for (int pass = q0 == 0 ? 0 : 1; pass < 2; ++pass) {
-    auto load = [&](int j0) {
-      const bf16* at = kv + (long long)j0 * ld;
-      tk.load(at, ld, len - j0, tid);
-      tv.load(at + DN, ld, len - j0, tid);
-      if constexpr (DR > 0) tp.load(pe + (long long)j0 * DR, DR, len - j0, tid);
-    };
     sum = 0.f;
-    load(0);
+    lds_barrier();  // all are done with the pass before
+    fetch(0, 0);
     for (int j0 = 0; j0 < keys; j0 += kK) {
-      __syncthreads();
-      tk.store(ks, tid);
-      tv.store(vs, tid);
-      if constexpr (DR > 0) tp.store(ks + DN, tid);
-      __syncthreads();
-      if (j0 + kK < keys) load(j0 + kK);
+      const int b = (j0 / kK) & 1;
+      const unsigned ks = base + b * (2 * kKey + kRot), vs = ks + kKey, rs = vs + kKey;
+      tile_barrier<0>();  // this tile is there, and all are done with the one before
+      if (j0 + kK < keys) fetch(j0 + kK, b ^ 1);
       if (j0 > w0 + 31) continue;
       f32x16 s = {}, dp = {};
 #pragma unroll
-      for (int k = 0; k < DQ / 16; ++k) s = mma(row_frag(ks + (lane & 31) * KP, k, half), qf[k], s);
+      for (int k = 0; k < DN / 16; ++k) {
+        s = mma(row_frag(ks, at, 0, k), qf[k], s);
+        dp = mma(row_frag(vs, at, 0, k), df[k], dp);
+      }
 #pragma unroll
-      for (int k = 0; k < DN / 16; ++k) dp = mma(row_frag(vs + (lane & 31) * VP, k, half), df[k], dp);
+      for (int k = 0; k < DR / 16; ++k) s = mma(row_frag(rs, at_rot, 0, k), qf[DN / 16 + k], s);
       const bool edge = j0 + kK - 1 > w0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -121,14 +102,17 @@ __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
       for (int k = 0; k < 2; ++k) {
         const bf16x8 sf = acc_frag(s, k);
 #pragma unroll
-        for (int d = 0; d < DQ / 32; ++d) acc[d] = mma(tr_frag<KP>(ks, 16 * k, 32 * d, lane), sf, acc[d]);
+        for (int d = 0; d < DN / 32; ++d) acc[d] = mma(tr_frag(ks, at, 16 * k, d), sf, acc[d]);
+#pragma unroll
+        for (int d = 0; d < DR / 32; ++d)
+          acc[DN / 32 + d] = mma(tr_frag(rs, at_rot, 16 * k, d), sf, acc[DN / 32 + d]);
       }
     }
     sum = halves_sum(sum);
     if (pass == 0) delta = sum;
   }
   if (!on) return;
-  if (half == 0) a.delta[row] = sum;
+  if (half == 0) *(f32x2*)(a.delta + 2 * row) = f32x2{lse, sum};
 #pragma unroll
   for (int d = 0; d < DQ / 32; ++d) {
     acc[d] *= a.scale;
@@ -144,14 +128,15 @@ __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
 // dK^T += Q^T dS.  The rotary part of dk is this head's share of dk_pe.
 template <int DN, int DR>
 __global__ __launch_bounds__(256, 1) void dkv_kernel(AttnArgs a, TileMap map) {
-  constexpr int DQ = DN + DR, QP = DQ + kPad, OP = DN + kPad;
-  __shared__ __align__(16) bf16 qs[kI * QP];
-  __shared__ __align__(16) bf16 os[kI * OP];
-  __shared__ __align__(16) float ls[kI], ds[kI];
+  constexpr int DQ = DN + DR;
+  // bytes of a tile's parts: queries, dout, the queries' rotary parts, and each wavefront's (lse, delta) rows
+  constexpr unsigned kQry = kI * DN * 2, kRot = kI * DR * 2, kStat = kI * 8, kTileBytes = 2 * kQry + kRot + 4 * kStat;
+  __shared__ __align__(1024) char lds[2][kTileBytes];
   int h, len, k0;
   long long t0;
   if (!tile_place<kRows>(a, map, false, h, t0, len, k0)) return;
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, w0 = k0 + (tid >> 6) * 32;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w0 = k0 + wave * 32;
   const int kj = w0 + (lane & 31);  // this lane's key
   const bool on = kj < len;
   const long long col = (t0 + kj) * a.H + h;
@@ -167,57 +152,59 @@ __global__ __launch_bounds__(256, 1) void dkv_kernel(AttnArgs a, TileMap map) {
   for (int s = 0; s < DR / 16; ++s) kf[DN / 16 + s] = on ? row_frag(a.k_pe + (t0 + kj) * DR, s, half) : bf16x8{};
   const float c = a.scale * kda::kLog2e;
 
-  Tile<kI, DQ, QP> tq;
-  Tile<kI, DN, OP> to;
-  float rl = 0.f, rd = 0.f;
-  auto load = [&](int i0) {
-    tq.load(a.q + (first + (long long)i0 * a.H) * DQ, a.H * DQ, len - i0, tid);
-    to.load(a.dout + (first + (long long)i0 * a.H) * DN, a.H * DN, len - i0, tid);
-    if (tid < kI) {
-      rl = rd = 0.f;  // past the document: q and do are zero, and so is what p weighs
-      if (i0 + tid < len) {
-        rl = a.lse[first + (long long)(i0 + tid) * a.H] * kda::kLog2e;
-        rd = a.delta[first + (long long)(i0 + tid) * a.H];
-      }
-    }
+  const unsigned base = lds_address(&lds[0][0]);
+  const LaneAt<DN> at(lane);
+  const LaneAt<64> at_rot(lane);
+  auto fetch = [&](int i0, int b) {
+    const unsigned to = base + b * kTileBytes;
+    const int last = len - 1 - i0;
+    const long long row = first + (long long)i0 * a.H;
+    fetch_rows<kI, DN>(a.q + row * DQ, a.H * DQ, last, to, wave, lane);
+    fetch_rows<kI, DN>(a.dout + row * DN, a.H * DN, last, to + kQry, wave, lane);
+    if constexpr (DR > 0) fetch_rows<kI, DR>(a.q + row * DQ + DN, a.H * DQ, last, to + 2 * kQry, wave, lane);
+    load_lds4(a.delta + 2 * row, (unsigned)(min(lane / 2, last) * (2 * a.H) + (lane & 1)) * 4,
+              to + 2 * kQry + kRot + wave * kStat);
   };
   f32x16 dk[DQ / 32] = {}, dv[DN / 32] = {};
-  load(k0);
+  fetch(k0, 0);
   for (int i0 = k0; i0 < len; i0 += kI) {
-    __syncthreads();
-    tq.store(qs, tid);
-    to.store(os, tid);
-    if (tid < kI) {
-      ls[tid] = rl;
-      ds[tid] = rd;
-    }
-    __syncthreads();
-    if (i0 + kI < len) load(i0 + kI);
+    const int b = ((i0 - k0) / kI) & 1;
+    const unsigned qs = base + b * kTileBytes, os = qs + kQry, rs = os + kQry, st = rs + kRot + wave * kStat;
+    tile_barrier<0>();  // this tile is there, and all are done with the one before
+    if (i0 + kI < len) fetch(i0 + kI, b ^ 1);
     if (i0 + kI - 1 < w0) continue;  // all of it is before this wavefront's keys
     f32x16 s = {}, dp = {};
 #pragma unroll
-    for (int k = 0; k < DQ / 16; ++k) s = mma(row_frag(qs + (lane & 31) * QP, k, half), kf[k], s);
+    for (int k = 0; k < DN / 16; ++k) {
+      s = mma(row_frag(qs, at, 0, k), kf[k], s);
+      dp = mma(row_frag(os, at, 0, k), vf[k], dp);
+    }
 #pragma unroll
-    for (int k = 0; k < DN / 16; ++k) dp = mma(row_frag(os + (lane & 31) * OP, k, half), vf[k], dp);
-    const bool edge = i0 < w0 + 31;
+    for (int k = 0; k < DR / 16; ++k) s = mma(row_frag(rs, at_rot, 0, k), kf[DN / 16 + k], s);
+    const bool edge = i0 < w0 + 31 || i0 + kI > len;
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const f32x4 lse = *(const f32x4*)(ls + acc_row(i, half)), del = *(const f32x4*)(ds + acc_row(i, half));
+    for (int i = 0; i < 16; i += 2) {
+      typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+      const f32x4 stat = *(const lds_f32x4*)(st + acc_row(i, half) * 8);  // lse, delta of two queries
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float p = kda::fast_exp2(__builtin_fmaf(s[i + e], c, -lse[e]));
-        if (edge && i0 + acc_row(i + e, half) < kj) p = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        float p = kda::fast_exp2(__builtin_fmaf(s[i + e], c, -stat[2 * e]));
+        const int qi = i0 + acc_row(i + e, half);
+        if (edge && (qi < kj || qi >= len)) p = 0.f;
         s[i + e] = p;
-        dp[i + e] = p * (dp[i + e] - del[e]);
+        dp[i + e] = p * (dp[i + e] - stat[2 * e + 1]);
       }
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const bf16x8 pf = acc_frag(s, k), sf = acc_frag(dp, k);
 #pragma unroll
-      for (int d = 0; d < DN / 32; ++d) dv[d] = mma(tr_frag<OP>(os, 16 * k, 32 * d, lane), pf, dv[d]);
+      for (int d = 0; d < DN / 32; ++d) dv[d] = mma(tr_frag(os, at, 16 * k, d), pf, dv[d]);
 #pragma unroll
-      for (int d = 0; d < DQ / 32; ++d) dk[d] = mma(tr_frag<QP>(qs, 16 * k, 32 * d, lane), sf, dk[d]);
+      for (int d = 0; d < DN / 32; ++d) dk[d] = mma(tr_frag(qs, at, 16 * k, d), sf, dk[d]);
+#pragma unroll
+      for (int d = 0; d < DR / 32; ++d)
+        dk[DN / 32 + d] = mma(tr_frag(rs, at_rot, 16 * k, d), sf, dk[DN / 32 + d]);
     }
   }
   if (!on) return;

@@ -4,6 +4,9 @@
 // the keys they see 64 at a time: S^T = K Q^T (the queries are B operands in
 // registers), the softmax's running maximum and sum a query a lane, then
 // O^T += V^T P^T, P from the accumulators of S^T without leaving the lane.
+// Keys and values go from memory straight into LDS, the next tile during a
+// tile; two workgroups a CU (2 x 80 KB of LDS at 128 / 64 channels) keep the
+// matrix units busy during the other's softmax.
 // Sums and statistics are float32; P is rounded to bf16 as an operand, the row
 // sum is taken before that.
 
@@ -18,19 +21,21 @@ constexpr int kQ = 128, kK = 64;  // queries of a workgroup, keys of a tile
 
 template <int DN, int DR>
 __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
-  constexpr int DQ = DN + DR, KP = DQ + kPad, VP = DN + kPad;
-  constexpr int kKv = 2 * DN / 8, kPe = DR / 8;             // 16-byte pieces of a row
-  constexpr int nKv = kK * kKv / 256, nPe = kK * kPe / 256;  // pieces a thread
-  __shared__ __align__(16) bf16 ks[kK * KP];
-  __shared__ __align__(16) bf16 vs[kK * VP];
+  constexpr int DQ = DN + DR;
+  constexpr unsigned kKey = kK * DN * 2, kRot = kK * DR * 2;  // bytes of a tile's parts: keys, values, rotary keys
+  __shared__ __align__(1024) char lds[2][2 * kKey + kRot];
   int h, len, q0;
   long long t0;
   if (!tile_place<kQ>(a, map, true, h, t0, len, q0)) return;
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, w0 = q0 + (tid >> 6) * 32;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w0 = q0 + wave * 32;
   const int qi = w0 + (lane & 31);  // this lane's query
   const int keys = min(len, q0 + kQ);
   const bf16* kv = a.kv + (t0 * a.H + h) * (2 * DN);
   const bf16* pe = a.k_pe + t0 * DR;
+  const unsigned base = lds_address(&lds[0][0]);
+  const LaneAt<DN> at(lane);
+  const LaneAt<64> at_rot(lane);
 
   bf16x8 qf[DQ / 16];
 #pragma unroll
@@ -38,51 +43,33 @@ __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
     qf[s] = bf16x8{};
     if (qi < len) qf[s] = row_frag(a.q + ((t0 + qi) * a.H + h) * DQ, s, half);
   }
-  u32x4 rkv[nKv], rpe[nPe ? nPe : 1];
-  auto load = [&](int j0) {
-#pragma unroll
-    for (int p = 0; p < nKv; ++p) {
-      const int row = (p * 256 + tid) / kKv, c = (p * 256 + tid) % kKv;
-      rkv[p] = u32x4{};
-      if (j0 + row < len) rkv[p] = *(const u32x4*)(kv + (long long)j0 * (a.H * 2 * DN) + row * (a.H * 2 * DN) + c * 8);
-    }
-    if constexpr (DR > 0) {
-#pragma unroll
-      for (int p = 0; p < nPe; ++p) {
-        const int row = (p * 256 + tid) / kPe, c = (p * 256 + tid) % kPe;
-        rpe[p] = u32x4{};
-        if (j0 + row < len) rpe[p] = *(const u32x4*)(pe + (long long)(j0 + row) * DR + c * 8);
-      }
-    }
-  };
-  auto store = [&]() {
-#pragma unroll
-    for (int p = 0; p < nKv; ++p) {
-      const int row = (p * 256 + tid) / kKv, c = (p * 256 + tid) % kKv;
-      *(u32x4*)(c < DN / 8 ? ks + row * KP + c * 8 : vs + row * VP + (c - DN / 8) * 8) = rkv[p];
-    }
-    if constexpr (DR > 0) {
-#pragma unroll
-      for (int p = 0; p < nPe; ++p)
-        *(u32x4*)(ks + ((p * 256 + tid) / kPe) * KP + DN + ((p * 256 + tid) % kPe) * 8) = rpe[p];
-    }
+  auto fetch = [&](int j0, int b) {
+    const unsigned to = base + b * (2 * kKey + kRot);
+    const bf16* from = kv + (long long)j0 * (a.H * 2 * DN);
+    fetch_rows<kK, DN>(from, a.H * 2 * DN, len - 1 - j0, to, wave, lane);
+    fetch_rows<kK, DN>(from + DN, a.H * 2 * DN, len - 1 - j0, to + kKey, wave, lane);
+    if constexpr (DR > 0) fetch_rows<kK, DR>(pe + (long long)j0 * DR, DR, len - 1 - j0, to + 2 * kKey, wave, lane);
   };
 
   f32x16 acc[DN / 32] = {};
   float m = -FLT_MAX, l = 0.f;  // running maximum of the scaled scores in log2 units; this lane's half of the sum
   const float c = a.scale * kda::kLog2e;
-  load(0);
+  fetch(0, 0);
   for (int j0 = 0; j0 < keys; j0 += kK) {
-    __syncthreads();
-    store();
-    __syncthreads();
-    if (j0 + kK < keys) load(j0 + kK);
+    const int b = (j0 / kK) & 1;
+    const unsigned ks = base + b * (2 * kKey + kRot), vs = ks + kKey, rs = vs + kKey;
+    tile_barrier<0>();  // this tile is there, and all are done with the one before
+    if (j0 + kK < keys) fetch(j0 + kK, b ^ 1);
     if (j0 > w0 + 31) continue;  // all of it is past this wavefront's queries
     f32x16 s[2] = {};
 #pragma unroll
-    for (int k = 0; k < DQ / 16; ++k)
+    for (int k = 0; k < DN / 16; ++k)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) s[u] = mma(row_frag(ks + (32 * u + (lane & 31)) * KP, k, half), qf[k], s[u]);
+      for (int u = 0; u < 2; ++u) s[u] = mma(row_frag(ks, at, 32 * u, k), qf[k], s[u]);
+#pragma unroll
+    for (int k = 0; k < DR / 16; ++k)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) s[u] = mma(row_frag(rs, at_rot, 32 * u, k), qf[DN / 16 + k], s[u]);
     if (j0 + kK - 1 > w0) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -116,7 +103,7 @@ __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
       for (int k = 0; k < 2; ++k) {
         const bf16x8 pf = acc_frag(s[u], k);
 #pragma unroll
-        for (int d = 0; d < DN / 32; ++d) acc[d] = mma(tr_frag<VP>(vs, 32 * u + 16 * k, 32 * d, lane), pf, acc[d]);
+        for (int d = 0; d < DN / 32; ++d) acc[d] = mma(tr_frag(vs, at, 32 * u + 16 * k, d), pf, acc[d]);
       }
     }
   }

@@ -57,7 +57,7 @@ struct AttnArgs {
   const int* cu;
   int N, T, H;       // documents; tokens of a batch row, or all of them with cu
   float scale;
-  float* delta;      // backward workspace: [tokens][H]
+  float* delta;      // backward workspace: [tokens][H][2], lse in log2 units and <dout, o>
   float* pe_part;    // backward workspace: [H][tokens][Dr]
   int tokens;
 };

@@ -79,25 +79,6 @@ __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int n) {
   return s;
 }
 
-// Waits until at most N of this wavefront's vector memory operations are on
-// their way (they end in order), and for the other wavefronts.
-template <int N>
-__device__ __forceinline__ void tile_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// 16 bytes a lane from global memory to lds + 16 lane (M0 holds the base; it
-// may not be read in the cycle after it is written).  Not seen by the
-// compiler's wait counts: tile_barrier waits for it.
-__device__ __forceinline__ void load_lds(const bf16* from, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from)
-               : "memory", "m0");
-}
-
 template <int R, int DR, int WQ>
 struct Paged {
   static constexpr bool PAIR = WQ < 4;  // two wavefronts for each 32 rows
@@ -172,16 +153,12 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   long long base = found[1];  // units before sequence n
   Sequence sq = sequence<C::kRows>(a, n);
   const float c = a.scale * kda::kLog2e;
-  const unsigned lds_lat = (unsigned)(size_t)(__attribute__((address_space(3))) char*)&lat[0][0];
-  const unsigned lds_rot = (unsigned)(size_t)(__attribute__((address_space(3))) char*)&rot[0][0];
+  const unsigned lds_lat = lds_address(&lat[0][0]), lds_rot = lds_address(&rot[0][0]);
 
-  // LDS addresses of this lane's fragments: row l32 of the latents and of the rotary keys, and the transposing
-  // read's row and column (tr_frag's places)
-  const int te = 4 * half + ((lane >> 2) & 3);
-  const unsigned at_k = l32 * (R * 2) + 32 * (lane & 7) + 16 * half;
-  const unsigned at_r = l32 * (DR * 2) + 32 * ((lane >> 1) & 3) + 16 * half;
-  const unsigned at_t = (R == 128 ? 0 : wd * R) + te * (R * 2) + (((((lane >> 4) & 1) ^ te) * 32) ^ (R == 128 ? 128 * wd : 0)) +
-                        ((lane >> 1) & 1) * 16 + (lane & 1) * 8;
+  const LaneAt<R> at_lat(lane);
+  const LaneAt<64> at_rot(lane);
+  LaneAt<R> at_out = at_lat;  // of the channels whose sums this wavefront holds
+  if constexpr (C::PAIR) at_out.col = R == 128 ? at_lat.col ^ 128 * wd : at_lat.col + R * wd;
 
   for (long long u = begin; u < end;) {
     while (u >= base + sq.units()) {
@@ -217,19 +194,29 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
     };
     // a tile into buffer b; rows that are not there read row 0 of the cache and are cleared later
     auto fetch = [&](const int* from, int b) {
-      constexpr int kPer = 512 / R;  // rows of one 1024-byte load
-#pragma unroll 4
-      for (int i = 0; i < kTile / kPer / C::kWaves; ++i) {
-        const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
-        const int piece = (lane % (R / 8)) ^ (2 * (r & 7));
-        load_lds(a.cache + (long long)max(from[r], 0) * D + piece * 8, lds_lat + (b * kTile + r0) * (R * 2));
+      constexpr int kPer = 512 / R, kN = kTile / kPer / C::kWaves;  // rows of one 1024-byte load, loads
+      if constexpr (R == 512) {  // a row a load: its address is scalar
+        const int mine = max(from[lane], 0);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int r = wave + C::kWaves * i;
+          load_lds(a.cache + (long long)__builtin_amdgcn_readlane(mine, r) * D, (lane ^ swizzle<R>(r)) * 16,
+                   lds_lat + (b * kTile + r) * (R * 2));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
+          load_lds_each(a.cache + (long long)max(from[r], 0) * D + ((lane % (R / 8)) ^ swizzle<R>(r)) * 8,
+                        lds_lat + (b * kTile + r0) * (R * 2));
+        }
       }
       if constexpr (DR > 0) {
 #pragma unroll
         for (int i = 0; i < 8 / C::kWaves; ++i) {
           const int r0 = (wave + C::kWaves * i) * 8, r = r0 + lane / 8;
-          const int piece = (lane % 8) ^ (2 * ((r >> 1) & 3));
-          load_lds(a.cache + (long long)max(from[r], 0) * D + R + piece * 8, lds_rot + (b * kTile + r0) * (DR * 2));
+          load_lds_each(a.cache + (long long)max(from[r], 0) * D + R + ((lane % 8) ^ swizzle<64>(r)) * 8,
+                        lds_rot + (b * kTile + r0) * (DR * 2));
         }
       }
     };
@@ -283,16 +270,11 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
         f32x16 s;
         auto scores = [&](int sub) {
           s = f32x16{};
-          // Rows are 256 bytes or a multiple: piece 2k of a row, permuted, is at the lane's address with bits
-          // XORed, so 8 addresses serve all k.
 #pragma unroll
-          for (int k = 0; k < R / 16; ++k)
-            s = mma(*(const lds_bf16x8*)(((lds_lat + (b * kTile + 32 * sub) * (R * 2) + at_k) ^ (32 * (k % 8))) + 256 * (k / 8)),
-                    qf[k], s);
+          for (int k = 0; k < R / 16; ++k) s = mma(row_frag(lds_lat + b * (kTile * R * 2), at_lat, 32 * sub, k), qf[k], s);
 #pragma unroll
           for (int k = 0; k < DR / 16; ++k)
-            s = mma(*(const lds_bf16x8*)((lds_rot + (b * kTile + 32 * sub) * (DR * 2) + at_r) ^ (32 * k)), qf[R / 16 + k],
-                    s);
+            s = mma(row_frag(lds_rot + b * (kTile * DR * 2), at_rot, 32 * sub, k), qf[R / 16 + k], s);
           if (!full) {
             const unsigned bits = (unsigned)(sees >> (32 * sub));
 #pragma unroll
@@ -327,11 +309,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
         auto values = [&](int sub, int k, bf16x8 pf) {
 #pragma unroll
           for (int d = 0; d < C::kOut; ++d) {
-            const unsigned at = ((lds_lat + (b * kTile + 32 * sub) * (R * 2) + at_t) ^ (64 * (d % 4))) + 256 * (d / 4) +
-                                16 * k * (R * 2);
-            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * R * 2));
-            acc[d] = mma(__builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), pf, acc[d]);
+            acc[d] = mma(tr_frag(lds_lat + b * (kTile * R * 2), at_out, 32 * sub + 16 * k, d), pf, acc[d]);
           }
         };
         bf16x8 pf[2];

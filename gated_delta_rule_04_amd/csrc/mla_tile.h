@@ -17,35 +17,106 @@
 namespace mla {
 
 using kda::bf16x8;
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+using kda::f32x2;
+using kda::f32x4;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kPad = 16;  // elements after each LDS row: 32 bytes, so that 8 rows' 16-byte reads and 4 rows'
-                          // 32-byte transposing reads fall on different banks for rows of 64, 128 and 192
-
 __device__ __forceinline__ f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// 16 inner values of a row-major LDS row: the lane's row, values 8h .. 8h+7.
+// 16 inner values of a row in global memory: values 8h .. 8h+7 of step s.
 __device__ __forceinline__ bf16x8 row_frag(const bf16* row, int s, int half) {
   return *(const bf16x8*)(row + 16 * s + 8 * half);
 }
 
-// A operand of M^T from a row-major tile M of row length P: its columns c0 ..
-// c0+31 as rows, over its rows r0 .. r0+15 in the accumulator's order.  In each
-// 16 lanes a transposing read takes 4 rows of 16 columns; lane 4e + q
-// addresses row e, columns 4q .. 4q+3.
-template <int P>
-__device__ __forceinline__ bf16x8 tr_frag(const bf16* tile, int r0, int c0, int lane) {
-  const bf16* lo = tile + (r0 + 4 * (lane >> 5) + ((lane >> 2) & 3)) * P + c0 + (lane & 16) + 4 * (lane & 3);
-  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+// Tiles in LDS: rows of W = 64 channels or 128 and more, without padding (the
+// loads from global memory straight into LDS write 1024 bytes in a row), the
+// 16-byte pieces of each row permuted instead: piece p of row r lies at p ^
+// swizzle(r).  The LDS serves 16 lanes of a 16-byte read together, and 32 of a
+// transposing one, from 64 banks; so 16 consecutive rows' equal pieces must lie
+// on 16 places of 256 bytes, and 4 consecutive rows' 64-byte runs on 4.
+template <int W>
+__device__ __forceinline__ constexpr int swizzle(int row) {
+  return W == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
+}
+
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+template <typename T>
+__device__ __forceinline__ unsigned lds_address(T* p) {
+  return (unsigned)(size_t)(__attribute__((address_space(3))) char*)p;
+}
+
+// Addresses of a lane's fragments, to be added to a tile's.
+//   row  of its row l % 32: step k is at (row ^ 32 (k % 8)) + 256 (k / 8)
+//   col  of the transposing read of rows 0 .. 15, columns 0 .. 31: columns 32d
+//        at (col ^ 64 (d % 4)) + 256 (d / 4); rows 8 further at 8 rows and ^ 32
+template <int W>
+struct LaneAt {
+  unsigned row, col;
+  __device__ __forceinline__ explicit LaneAt(int lane) {
+    const int r = lane & 31, half = lane >> 5, t = 4 * half + ((lane >> 2) & 3);
+    row = r * (W * 2) + (half ^ swizzle<W>(r)) * 16;
+    col = t * (W * 2) + ((2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ swizzle<W>(t)) * 16 + (lane & 1) * 8;
+  }
+};
+template <int W>
+__device__ __forceinline__ bf16x8 row_frag(unsigned tile, const LaneAt<W>& at, int r0, int k) {
+  return *(const lds_bf16x8*)(((tile + r0 * (W * 2) + at.row) ^ (32 * (k % 8))) + 256 * (k / 8));
+}
+// A operand of M^T from a tile M: its columns 32d .. 32d+31 as rows, over its
+// rows r0 .. r0+15 in the accumulator's order.  In each 16 lanes a transposing
+// read takes 4 rows of 16 columns; lane 4e + q addresses row e, columns 4q ..
+// 4q+3.
+template <int W>
+__device__ __forceinline__ bf16x8 tr_frag(unsigned tile, const LaneAt<W>& at, int r0, int d) {
+  const unsigned lo = ((tile + r0 * (W * 2) + at.col) ^ (64 * (d % 4))) + 256 * (d / 4);
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)lo);
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lo + 8 * P));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)((lo ^ 32) + 8 * (W * 2)));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// 16 (or 4) bytes a lane from base + off straight to lds + 16 (4) lane.  M0
+// holds the LDS address; it may not be read in the cycle after it is written.
+// The compiler's wait counts do not see these loads: tile_barrier waits for
+// them, and nothing else may read what they write.
+__device__ __forceinline__ void load_lds(const void* base, unsigned off, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+// The same with an address a lane.
+__device__ __forceinline__ void load_lds_each(const bf16* from, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(const void* base, unsigned off, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+// Waits until at most N of this wavefront's vector memory operations are on
+// their way (they end in order), and for the other wavefronts.
+template <int N>
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Rows 0 .. ROWS-1 of W channels from a strided tensor into a tile, by 4
+// wavefronts; rows after `last` read it again (their weights are zero).
+template <int ROWS, int W>
+__device__ __forceinline__ void fetch_rows(const bf16* base, int stride, int last, unsigned tile, int wave, int lane) {
+  constexpr int kPer = 512 / W, kN = ROWS / kPer;  // rows of one 1024-byte load, loads
+  static_assert(kN % 4 == 0, "each wavefront has the same number of loads");
+#pragma unroll
+  for (int i = 0; i < kN / 4; ++i) {
+    const int r0 = (wave + 4 * i) * kPer, r = r0 + lane / (W / 8);
+    load_lds(base, (unsigned)(min(r, last) * stride + ((lane % (W / 8)) ^ swizzle<W>(r)) * 8) * 2, tile + r0 * (W * 2));
+  }
 }
 
 // Registers 8s .. 8s+7 of an accumulator as a B operand.

@@ -518,7 +518,7 @@ kda_status kda_mla_attn_fwd(const void* q, const void* kv, const void* k_pe, voi
                             const int* cu_seqlens, int num_seqs, int B, int T, int H, int Dn, int Dr, int Dv,
                             float scale, kda_dtype dt, void* stream);
 
-/* Bytes of device workspace kda_mla_attn_bwd needs: each row's <dout, o>, and
+/* Bytes of device workspace kda_mla_attn_bwd needs: two statistics a row, and
  * each head's share of the shared rotary key's gradient (float32).  0 for
  * invalid sizes. */
 size_t kda_mla_attn_bwd_workspace_bytes(int B, int T, int H, int Dn, int Dr, int Dv, int num_seqs, kda_dtype dt);
