@@ -89,11 +89,14 @@ __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
       }
 #pragma unroll
       for (int k = 0; k < DR / 16; ++k) s = mma(row_frag(rs, at_rot, 0, k), qf[DN / 16 + k], s);
-      const bool edge = j0 + kK - 1 > w0;
+      if (j0 + kK - 1 > w0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (j0 + acc_row(i, half) > qi) s[i] = -INFINITY;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float p = kda::fast_exp2(__builtin_fmaf(s[i], c, -lse));
-        if (edge && j0 + acc_row(i, half) > qi) p = 0.f;
+        const float p = kda::fast_exp2(__builtin_fmaf(s[i], c, -lse));
         sum = __builtin_fmaf(p, dp[i], sum);
         s[i] = p * (dp[i] - delta);
       }
@@ -131,7 +134,8 @@ __global__ __launch_bounds__(256, 1) void dkv_kernel(AttnArgs a, TileMap map) {
   constexpr int DQ = DN + DR;
   // bytes of a tile's parts: queries, dout, the queries' rotary parts, and each wavefront's (lse, delta) rows
   constexpr unsigned kQry = kI * DN * 2, kRot = kI * DR * 2, kStat = kI * 8, kTileBytes = 2 * kQry + kRot + 4 * kStat;
-  __shared__ __align__(1024) char lds[2][kTileBytes];
+  constexpr int kLoads = (2 * kQry + kRot) / 4096 + 1;  // a wavefront's share of a tile
+  __shared__ __align__(1024) char lds[3][kTileBytes];
   int h, len, k0;
   long long t0;
   if (!tile_place<kRows>(a, map, false, h, t0, len, k0)) return;
@@ -166,14 +170,12 @@ __global__ __launch_bounds__(256, 1) void dkv_kernel(AttnArgs a, TileMap map) {
               to + 2 * kQry + kRot + wave * kStat);
   };
   f32x16 dk[DQ / 32] = {}, dv[DN / 32] = {};
-  fetch(k0, 0);
-  for (int i0 = k0; i0 < len; i0 += kI) {
-    const int b = ((i0 - k0) / kI) & 1;
-    const unsigned qs = base + b * kTileBytes, os = qs + kQry, rs = os + kQry, st = rs + kRot + wave * kStat;
-    tile_barrier<0>();  // this tile is there, and all are done with the one before
-    if (i0 + kI < len) fetch(i0 + kI, b ^ 1);
-    if (i0 + kI - 1 < w0) continue;  // all of it is before this wavefront's keys
-    f32x16 s = {}, dp = {};
+  // The scores of the next tile are formed beside the weights of this one, so
+  // that matrix and vector work of one wavefront overlap.
+  auto scores = [&](int b, f32x16& s, f32x16& dp) {
+    const unsigned qs = base + b * kTileBytes, os = qs + kQry, rs = os + kQry;
+    s = f32x16{};
+    dp = f32x16{};
 #pragma unroll
     for (int k = 0; k < DN / 16; ++k) {
       s = mma(row_frag(qs, at, 0, k), kf[k], s);
@@ -181,18 +183,39 @@ __global__ __launch_bounds__(256, 1) void dkv_kernel(AttnArgs a, TileMap map) {
     }
 #pragma unroll
     for (int k = 0; k < DR / 16; ++k) s = mma(row_frag(rs, at_rot, 0, k), kf[DN / 16 + k], s);
-    const bool edge = i0 < w0 + 31 || i0 + kI > len;
+  };
+  const int tiles = (len - k0 + kI - 1) / kI;
+  f32x16 s, dp;
+  fetch(k0, 0);
+  if (tiles > 1) fetch(k0 + kI, 1);
+  if (tiles > 1)
+    tile_barrier<kLoads>();
+  else
+    tile_barrier<0>();
+  scores(0, s, dp);
+  int b = 0;  // buffer of tile t, of 3
+  for (int t = 0; t < tiles; ++t) {
+    const int i0 = k0 + t * kI, b1 = b == 2 ? 0 : b + 1, b2 = b1 == 2 ? 0 : b1 + 1;
+    const unsigned qs = base + b * kTileBytes, os = qs + kQry, rs = os + kQry, st = rs + kRot + wave * kStat;
+    tile_barrier<0>();  // the next tile is there, and all are done with the one before
+    if (t + 2 < tiles) fetch(i0 + 2 * kI, b2);
+    if (i0 < w0 + 31 || i0 + kI > len) {  // queries before the key, and past the document
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int qi = i0 + acc_row(i, half);
+        if (qi < kj || qi >= len) s[i] = -INFINITY;
+      }
+    }
+    f32x16 s1, dp1;
+    scores(t + 1 < tiles ? b1 : b, s1, dp1);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
       const f32x4 stat = *(const lds_f32x4*)(st + acc_row(i, half) * 8);  // lse, delta of two queries
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float p = kda::fast_exp2(__builtin_fmaf(s[i + e], c, -stat[2 * e]));
-        const int qi = i0 + acc_row(i + e, half);
-        if (edge && (qi < kj || qi >= len)) p = 0.f;
-        s[i + e] = p;
-        dp[i + e] = p * (dp[i + e] - stat[2 * e + 1]);
+        s[i + e] = kda::fast_exp2(__builtin_fmaf(s[i + e], c, -stat[2 * e]));
+        dp[i + e] = s[i + e] * (dp[i + e] - stat[2 * e + 1]);
       }
     }
 #pragma unroll
@@ -206,6 +229,9 @@ __global__ __launch_bounds__(256, 1) void dkv_kernel(AttnArgs a, TileMap map) {
       for (int d = 0; d < DR / 32; ++d)
         dk[DN / 32 + d] = mma(tr_frag(rs, at_rot, 16 * k, d), sf, dk[DN / 32 + d]);
     }
+    s = s1;
+    dp = dp1;
+    b = b1;
   }
   if (!on) return;
 #pragma unroll

@@ -466,8 +466,8 @@ hipError_t launch(const PagedWork& w, const PagedPlan& p, hipStream_t stream) {
   paged_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w);
   if (p.groups > 1) {
     const long long rows = (long long)w.a.Tq * w.a.H;
-    // parts a block can have: with more than 4 a row takes several workgroups
-    if (p.groups > 4 * (rows / C::kRows + 1))
+    // parts a block can have: with more than 8 a row takes several workgroups
+    if (p.groups > 8 * (rows / C::kRows + 1))
       combine_kernel<R, C::kRows, true><<<dim3((unsigned)(rows * (R / 128))), dim3(256), 0, stream>>>(w, p.groups);
     else
       combine_kernel<R, C::kRows, false><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(w, p.groups);
