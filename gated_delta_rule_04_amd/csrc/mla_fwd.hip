@@ -23,7 +23,7 @@ template <int DN, int DR>
 __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
   constexpr int DQ = DN + DR;
   constexpr unsigned kKey = kK * DN * 2, kRot = kK * DR * 2;  // bytes of a tile's parts: keys, values, rotary keys
-  __shared__ __align__(1024) char lds[2][2 * kKey + kRot];
+  __shared__ __align__(1024) char lds[2 * (2 * kKey + kRot)];  // keys of 2 tiles, values of 2
   int h, len, q0;
   long long t0;
   if (!tile_place<kQ>(a, map, true, h, t0, len, q0)) return;
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
   const int keys = min(len, q0 + kQ);
   const bf16* kv = a.kv + (t0 * a.H + h) * (2 * DN);
   const bf16* pe = a.k_pe + t0 * DR;
-  const unsigned base = lds_address(&lds[0][0]);
+  const unsigned base = lds_address(lds);
   const LaneAt<DN> at(lane);
   const LaneAt<64> at_rot(lane);
 
@@ -43,25 +43,22 @@ __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
     qf[s] = bf16x8{};
     if (qi < len) qf[s] = row_frag(a.q + ((t0 + qi) * a.H + h) * DQ, s, half);
   }
-  auto fetch = [&](int j0, int b) {
-    const unsigned to = base + b * (2 * kKey + kRot);
-    const bf16* from = kv + (long long)j0 * (a.H * 2 * DN);
-    fetch_rows<kK, DN>(from, a.H * 2 * DN, len - 1 - j0, to, wave, lane);
-    fetch_rows<kK, DN>(from + DN, a.H * 2 * DN, len - 1 - j0, to + kKey, wave, lane);
-    if constexpr (DR > 0) fetch_rows<kK, DR>(pe + (long long)j0 * DR, DR, len - 1 - j0, to + 2 * kKey, wave, lane);
+  // A tile's keys are needed a tile before its values.
+  constexpr unsigned kTileKey = kKey + kRot;
+  auto fetch_keys = [&](int t) {
+    const unsigned to = base + (t & 1) * kTileKey;
+    const long long j0 = (long long)t * kK;
+    fetch_rows<kK, DN>(kv + j0 * (a.H * 2 * DN), a.H * 2 * DN, (int)(len - 1 - j0), to, wave, lane);
+    if constexpr (DR > 0) fetch_rows<kK, DR>(pe + j0 * DR, DR, (int)(len - 1 - j0), to + kKey, wave, lane);
   };
-
-  f32x16 acc[DN / 32] = {};
-  float m = -FLT_MAX, l = 0.f;  // running maximum of the scaled scores in log2 units; this lane's half of the sum
-  const float c = a.scale * kda::kLog2e;
-  fetch(0, 0);
-  for (int j0 = 0; j0 < keys; j0 += kK) {
-    const int b = (j0 / kK) & 1;
-    const unsigned ks = base + b * (2 * kKey + kRot), vs = ks + kKey, rs = vs + kKey;
-    tile_barrier<0>();  // this tile is there, and all are done with the one before
-    if (j0 + kK < keys) fetch(j0 + kK, b ^ 1);
-    if (j0 > w0 + 31) continue;  // all of it is past this wavefront's queries
-    f32x16 s[2] = {};
+  auto fetch_values = [&](int t) {
+    const long long j0 = (long long)t * kK;
+    fetch_rows<kK, DN>(kv + j0 * (a.H * 2 * DN) + DN, a.H * 2 * DN, (int)(len - 1 - j0),
+                       base + 2 * kTileKey + (t & 1) * kKey, wave, lane);
+  };
+  auto scores = [&](int t, f32x16* s) {
+    const unsigned ks = base + (t & 1) * kTileKey, rs = ks + kKey;
+    s[0] = s[1] = f32x16{};
 #pragma unroll
     for (int k = 0; k < DN / 16; ++k)
 #pragma unroll
@@ -70,6 +67,27 @@ __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
     for (int k = 0; k < DR / 16; ++k)
 #pragma unroll
       for (int u = 0; u < 2; ++u) s[u] = mma(row_frag(rs, at_rot, 32 * u, k), qf[DN / 16 + k], s[u]);
+  };
+
+  f32x16 acc[DN / 32] = {}, s[2];
+  float m = -FLT_MAX, l = 0.f;  // running maximum of the scaled scores in log2 units; this lane's half of the sum
+  const float c = a.scale * kda::kLog2e;
+  const int tiles = (keys + kK - 1) / kK;
+  constexpr int kLoads = (2 * kKey + kRot) / 4096;  // a wavefront's share of a tile's keys and values
+  fetch_keys(0);
+  if (tiles > 1) fetch_keys(1);
+  fetch_values(0);
+  if (tiles > 1)
+    tile_barrier<kLoads>();
+  else
+    tile_barrier<kKey / 4096>();
+  scores(0, s);
+  for (int t = 0; t < tiles; ++t) {
+    const int j0 = t * kK;
+    tile_barrier<0>();  // these values and the next keys are there, and all are done with the tile before
+    if (t + 2 < tiles) fetch_keys(t + 2);
+    if (t + 1 < tiles) fetch_values(t + 1);
+    if (j0 > w0 + 31) continue;  // all of it is past this wavefront's queries
     if (j0 + kK - 1 > w0) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -92,6 +110,12 @@ __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
 #pragma unroll
       for (int d = 0; d < DN / 32; ++d) acc[d] *= f;
     }
+    // The next tile's scores are formed beside this tile's weights, so that
+    // matrix and vector work overlap (after the last tile: of what is there,
+    // and not used).
+    f32x16 s1[2];
+    scores(t + 1, s1);
+    const unsigned vs = base + 2 * kTileKey + (t & 1) * kKey;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -106,6 +130,8 @@ __global__ __launch_bounds__(256, 2) void fwd_kernel(AttnArgs a, TileMap map) {
         for (int d = 0; d < DN / 32; ++d) acc[d] = mma(tr_frag(vs, at, 32 * u + 16 * k, d), pf, acc[d]);
       }
     }
+    s[0] = s1[0];
+    s[1] = s1[1];
   }
   l = halves_sum(l);
   if (qi >= len) return;
