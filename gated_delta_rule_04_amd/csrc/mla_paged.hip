@@ -84,6 +84,8 @@ struct Paged {
   static constexpr bool PAIR = WQ < 4;  // two wavefronts for each 32 rows
   static constexpr int D = R + DR, kWaves = PAIR ? 2 * WQ : WQ, kThreads = 64 * kWaves;
   static constexpr int kRows = 32 * WQ;
+  static constexpr int kLatLoads = kTile * R / 512 / kWaves, kRotLoads = DR ? 8 / kWaves : 0;  // a wavefront's share
+  static constexpr int kSubs = PAIR ? 1 : 2;  // 32-row halves of a tile whose scores a wavefront forms
   static constexpr int kOut = PAIR ? R / 64 : R / 32;  // 32-channel tiles of O a wavefront holds
 };
 
@@ -122,33 +124,33 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
     __syncthreads();
     return x + before;
   };
-  long long total = 0;
+  long long total = 0, mine_units = 0, incl = 0;
   for (int n0 = 0; n0 < a.N; n0 += C::kThreads) {
     const int n = n0 + tid;
-    const long long mine = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
-    const long long incl = block_scan(mine) + total;
-    if (blockIdx.x == 0 && n < a.N) w.prefix[n] = incl - mine;
+    mine_units = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
+    incl = block_scan(mine_units) + total;
+    if (blockIdx.x == 0 && n < a.N) w.prefix[n] = incl - mine_units;
     total += scan[C::kWaves];
   }
   if (blockIdx.x == 0 && tid == 0) w.prefix[a.N] = total;
   const long long share = (total + gridDim.x - 1) / gridDim.x;
   const long long begin = share * blockIdx.x, end = min(begin + share, total);
   if (begin >= end) return;
-  {
-    long long before = 0;
-    for (int n0 = 0; n0 < a.N; n0 += C::kThreads) {
+  long long before = 0;
+  for (int n0 = 0; n0 < a.N; n0 += C::kThreads) {
+    if (a.N > C::kThreads) {
       const int n = n0 + tid;
-      const long long mine = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
-      const long long incl = block_scan(mine) + before;
-      if (incl - mine <= begin && begin < incl) {
-        found[0] = n;
-        found[1] = incl - mine;
-      }
+      mine_units = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
+      incl = block_scan(mine_units) + before;
       before += scan[C::kWaves];
-      if (begin < before) break;
     }
-    __syncthreads();
+    if (incl - mine_units <= begin && begin < incl) {
+      found[0] = n0 + tid;
+      found[1] = incl - mine_units;
+    }
+    if (begin < before) break;
   }
+  __syncthreads();
   int n = (int)found[0];
   long long base = found[1];  // units before sequence n
   Sequence sq = sequence<C::kRows>(a, n);
@@ -192,35 +194,22 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
         places[e] = r;
       }
     };
-    // a tile into buffer b; rows that are not there read row 0 of the cache and are cleared later
-    auto fetch = [&](const int* from, int b) {
-      constexpr int kPer = 512 / R, kN = kTile / kPer / C::kWaves;  // rows of one 1024-byte load, loads
-      if constexpr (R == 512) {  // a row a load: its address is scalar
-        const int mine = max(from[lane], 0);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int r = wave + C::kWaves * i;
-          load_lds(a.cache + (long long)__builtin_amdgcn_readlane(mine, r) * D, (lane ^ swizzle<R>(r)) * 16,
-                   lds_lat + (b * kTile + r) * (R * 2));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
-          load_lds_each(a.cache + (long long)max(from[r], 0) * D + ((lane % (R / 8)) ^ swizzle<R>(r)) * 8,
-                        lds_lat + (b * kTile + r0) * (R * 2));
-        }
-      }
-      if constexpr (DR > 0) {
-#pragma unroll
-        for (int i = 0; i < 8 / C::kWaves; ++i) {
-          const int r0 = (wave + C::kWaves * i) * 8, r = r0 + lane / 8;
-          load_lds_each(a.cache + (long long)max(from[r], 0) * D + R + ((lane % 8) ^ swizzle<64>(r)) * 8,
-                        lds_rot + (b * kTile + r0) * (DR * 2));
-        }
-      }
+    // Load i of this wavefront's share of a tile's latents, or of its rotary keys, into buffer b; rows that are not
+    // there read row 0 of the cache and are cleared later.  `from` is the place of row `lane` of the tile.
+    auto fetch_lat = [&](int i, int from, int b, unsigned long long on) {
+      constexpr int kPer = 512 / R;  // rows of one 1024-byte load
+      const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
+      const unsigned to = lds_lat + (b * kTile + r0) * (R * 2);
+      if constexpr (R == 512)  // a row a load: its address is scalar
+        load_lds_if(on, a.cache + (long long)__builtin_amdgcn_readlane(from, r0) * D, (lane ^ swizzle<R>(r0)) * 16, to);
+      else
+        load_lds_if(on, a.cache + (long long)__shfl(from, r) * D + ((lane % (R / 8)) ^ swizzle<R>(r)) * 8, to);
     };
-    constexpr int kLoads = (kTile * R / 512 + (DR ? 8 : 0)) / C::kWaves;  // a wavefront's share of a tile
+    auto fetch_rot = [&](int i, int from, int b, unsigned long long on) {
+      const int r0 = (wave + C::kWaves * i) * 8, r = r0 + lane / 8;
+      load_lds_if(on, a.cache + (long long)__shfl(from, r) * D + R + ((lane % 8) ^ swizzle<64>(r)) * 8,
+                  lds_rot + (b * kTile + r0) * (DR * 2));
+    };
 
     f32x16 acc[C::kOut] = {};
     float m = -FLT_MAX, l = 0.f;
@@ -232,27 +221,21 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
       __syncthreads();  // the run before is done with the buffers
       look_up(p0);
       __syncthreads();
-      fetch(places, 0);
-      if (t0 + 1 < stop) fetch(places + kTile, 1);
-      unsigned long long next = __ballot(places[lane] >= 0);
+      int mine = places[lane];
+#pragma unroll
+      for (int i = 0; i < C::kLatLoads; ++i) fetch_lat(i, max(mine, 0), 0, ~0ull);
+#pragma unroll
+      for (int i = 0; i < C::kRotLoads; ++i) fetch_rot(i, max(mine, 0), 0, ~0ull);
       for (int t = t0; t < stop; ++t) {
         const int b = (t - t0) & 1;
-        if (t > t0) {  // the buffer of tile t - 1 is free: tile t + 1 into it
+        const unsigned long long there = __ballot(mine >= 0);
+        if (t + 1 == p0 + kPlaces) {
           lds_barrier();
-          if (t + 1 < stop) {
-            if (t + 1 == p0 + kPlaces) {
-              look_up(p0 = t + 1);
-              lds_barrier();
-            }
-            fetch(places + (t + 1 - p0) * kTile, b ^ 1);
-          }
+          look_up(p0 = t + 1);
         }
-        if (t + 1 < stop)  // tile t is there, tile t + 1 on its way
-          tile_barrier<kLoads>();
-        else
-          tile_barrier<0>();
-        const unsigned long long there = next;
-        if (t + 1 < stop) next = __ballot(places[(t + 1 - p0) * kTile + lane] >= 0);
+        tile_barrier<0>();  // tile t is there, and all are done with tile t - 1
+        if (t + 1 < stop) mine = places[(t + 1 - p0) * kTile + lane];
+        const unsigned long long more = t + 1 < stop ? ~0ull : 0ull;
         if (there != ~0ull) {  // uniform: every wavefront has the same 64 places
           for (int e = tid; e < kTile * (D / 8); e += C::kThreads) {
             const int r = e / (D / 8), piece = e % (D / 8);
@@ -261,20 +244,37 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
           }
           lds_barrier();
         }
-        if (!C::PAIR && m0 >= rows) continue;
+        const int from = max(mine, 0);
+        if (!C::PAIR && m0 >= rows) {  // no rows: only this wavefront's share of the next tile
+#pragma unroll
+          for (int i = 0; i < C::kLatLoads; ++i) fetch_lat(i, from, b ^ 1, more);
+#pragma unroll
+          for (int i = 0; i < C::kRotLoads; ++i) fetch_rot(i, from, b ^ 1, more);
+          continue;
+        }
         const long long span = (long long)lim - (long long)t * kTile;  // the lane's row sees tile rows 0 .. span
         unsigned long long sees = there & (span < 0 ? 0ull : span >= 63 ? ~0ull : (2ull << span) - 1);
         const bool full = __all(sees == ~0ull);
         sees >>= 4 * half;
         // S^T of 32 rows of the tile, scaled to log2 units later; masked rows at -infinity; its maximum a query
         f32x16 s;
-        auto scores = [&](int sub) {
+        // The next tile's loads are put between the products, a few at a time: the memory system takes a tile no
+        // faster than it delivers one, and a wavefront that issues all of its share at once waits for that.
+        constexpr int kLat = C::kLatLoads / C::kSubs, kRot = C::kRotLoads / C::kSubs, kShare = kLat + kRot;
+        auto scores = [&](int sub, int part) {
           s = f32x16{};
 #pragma unroll
-          for (int k = 0; k < R / 16; ++k) s = mma(row_frag(lds_lat + b * (kTile * R * 2), at_lat, 32 * sub, k), qf[k], s);
+          for (int k = 0; k < D / 16; ++k) {
+            s = mma(k < R / 16 ? row_frag(lds_lat + b * (kTile * R * 2), at_lat, 32 * sub, k)
+                               : row_frag(lds_rot + b * (kTile * DR * 2), at_rot, 32 * sub, k - R / 16),
+                    qf[k], s);
 #pragma unroll
-          for (int k = 0; k < DR / 16; ++k)
-            s = mma(row_frag(lds_rot + b * (kTile * DR * 2), at_rot, 32 * sub, k), qf[R / 16 + k], s);
+            for (int i = k * kShare / (D / 16); i < (k + 1) * kShare / (D / 16); ++i)
+              if (i < kLat)
+                fetch_lat(part * kLat + i, from, b ^ 1, more);
+              else
+                fetch_rot(part * kRot + i - kLat, from, b ^ 1, more);
+          }
           if (!full) {
             const unsigned bits = (unsigned)(sees >> (32 * sub));
 #pragma unroll
@@ -316,7 +316,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
         if constexpr (C::PAIR) {
           // The weights are handed over as they come with the pair's present reference, and formed again only
           // where a maximum rose past it: one barrier a tile.
-          const float mx = scores(wd);
+          const float mx = scores(wd, 0);
           const bool over = mx > m + 8.f;
           float sum = weights(s, pf);
           rise[wd][32 * wq + l32] = over ? mx : -FLT_MAX;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
         } else {
 #pragma unroll 1
           for (int sub = 0; sub < 2; ++sub) {
-            const float mx = scores(sub);
+            const float mx = scores(sub, sub);
             if (__any(mx > m + 8.f)) refer(mx);
             l += weights(s, pf);
             values(sub, 0, pf[0]);

@@ -81,22 +81,39 @@ __device__ __forceinline__ bf16x8 tr_frag(unsigned tile, const LaneAt<W>& at, in
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// 16 (or 4) bytes a lane from base + off straight to lds + 16 (4) lane.  M0
-// holds the LDS address; it may not be read in the cycle after it is written.
-// The compiler's wait counts do not see these loads: tile_barrier waits for
-// them, and nothing else may read what they write.
-__device__ __forceinline__ void load_lds(const void* base, unsigned off, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
+// A value that is the same in all lanes, as a scalar.
+__device__ __forceinline__ unsigned uniform(unsigned x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ unsigned long long uniform(unsigned long long x) {
+  return (unsigned long long)uniform((unsigned)(x >> 32)) << 32 | uniform((unsigned)x);
 }
-// The same with an address a lane.
-__device__ __forceinline__ void load_lds_each(const bf16* from, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from)
-               : "memory", "m0");
+
+// 16 (or 4) bytes a lane from base + off straight to lds + 16 (4) lane.  M0
+// holds the LDS address; it may not be read by the instruction after the one
+// that writes it.  The compiler's wait counts do not see these loads, nor that
+// they write LDS: tile_barrier waits for them and orders what reads it.
+__device__ __forceinline__ void load_lds(const void* base, unsigned off, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(lds)), "v"(off),
+               "s"(uniform((unsigned long long)base))
+               : "m0");
 }
 __device__ __forceinline__ void load_lds4(const void* base, unsigned off, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(uniform(lds)), "v"(off),
+               "s"(uniform((unsigned long long)base))
+               : "m0");
+}
+// The same for the lanes of `on` (all lanes are active before and after), and
+// with an address a lane.
+__device__ __forceinline__ void load_lds_if(unsigned long long on, const void* base, unsigned off, unsigned lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1" ::"s"(uniform(lds)),
+      "v"(off), "s"(uniform((unsigned long long)base)), "s"(uniform(on))
+      : "m0");
+}
+__device__ __forceinline__ void load_lds_if(unsigned long long on, const bf16* from, unsigned lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_mov_b64 exec, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1" ::"s"(uniform(lds)),
+      "v"(from), "s"(uniform(on))
+      : "m0");
 }
 // Waits until at most N of this wavefront's vector memory operations are on
 // their way (they end in order), and for the other wavefronts.
