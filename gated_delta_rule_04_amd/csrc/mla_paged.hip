@@ -8,11 +8,12 @@
 // row sum) that combine_kernel joins.  The split depends on the sizes and
 // lengths alone, and the parts are joined in order.
 //
-// A wavefront owns 32 query rows: S^T = C Q^T with the queries as B operands
-// in registers, the softmax a row a lane, O^T += C^T P^T with all R channels
-// of O^T in accumulators (256 registers at R = 512), so wavefronts share
-// nothing but the tile.  With few rows two wavefronts take the two halves of
-// each tile for the same rows and are joined at the end of a run.
+// A workgroup has 4 wavefronts.  S^T = C Q^T with the queries as B operands in
+// registers, the softmax a row a lane, O^T += C^T P^T.  With 128 rows a
+// wavefront owns 32 of them and all R channels of O^T (256 registers of sums
+// at R = 512), and shares nothing but the tile; with 64 or 32 rows, two or
+// four wavefronts own the same rows: each forms the scores of half the tile
+// and the sums of its share of the channels, the weights going through LDS.
 // Tiles come from the pages straight into LDS (no registers pass through),
 // the next one on its way during a tile, 16-byte pieces permuted within a row
 // so that both the row reads and the transposing reads spread over the banks.
@@ -81,12 +82,11 @@ __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int n) {
 
 template <int R, int DR, int WQ>
 struct Paged {
-  static constexpr bool PAIR = WQ < 4;  // two wavefronts for each 32 rows
-  static constexpr int D = R + DR, kWaves = PAIR ? 2 * WQ : WQ, kThreads = 64 * kWaves;
-  static constexpr int kRows = 32 * WQ;
+  static constexpr int WD = 4 / WQ;  // wavefronts for each 32 rows
+  static constexpr int D = R + DR, kWaves = 4, kThreads = 64 * kWaves, kRows = 32 * WQ;
   static constexpr int kLatLoads = kTile * R / 512 / kWaves, kRotLoads = DR ? 8 / kWaves : 0;  // a wavefront's share
-  static constexpr int kSubs = PAIR ? 1 : 2;  // 32-row halves of a tile whose scores a wavefront forms
-  static constexpr int kOut = PAIR ? R / 64 : R / 32;  // 32-channel tiles of O a wavefront holds
+  static constexpr int kSubs = WD > 1 ? 1 : 2;  // 32-row halves of a tile whose scores a wavefront forms
+  static constexpr int kOut = R / 32 / WD;  // 32-channel tiles of O a wavefront holds
 };
 
 template <int R, int DR, int WQ>
@@ -98,7 +98,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   __shared__ long long scan[C::kWaves + 1];
   __shared__ long long found[2];
   __shared__ int places[kPlaces * kTile];
-  __shared__ __align__(16) u32x4 handed[C::PAIR ? C::kWaves : 1][2][64];  // a pair's weights, as B operands
+  __shared__ __align__(16) u32x4 handed[C::WD > 1 ? WQ : 1][2][2][64];  // weights of the tile's halves, as B operands
   __shared__ float rise[2][C::kRows], sums[2][C::kRows];
   const PagedArgs& a = w.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
@@ -160,7 +160,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   const LaneAt<R> at_lat(lane);
   const LaneAt<64> at_rot(lane);
   LaneAt<R> at_out = at_lat;  // of the channels whose sums this wavefront holds
-  if constexpr (C::PAIR) at_out.col = R == 128 ? at_lat.col ^ 128 * wd : at_lat.col + R * wd;
+  at_out.col = (at_lat.col ^ (64 * (wd * C::kOut % 4))) + 256 * (wd * C::kOut / 4);
 
   for (long long u = begin; u < end;) {
     while (u >= base + sq.units()) {
@@ -245,7 +245,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
           lds_barrier();
         }
         const int from = max(mine, 0);
-        if (!C::PAIR && m0 >= rows) {  // no rows: only this wavefront's share of the next tile
+        if (C::WD == 1 && m0 >= rows) {  // no rows: only this wavefront's share of the next tile
 #pragma unroll
           for (int i = 0; i < C::kLatLoads; ++i) fetch_lat(i, from, b ^ 1, more);
 #pragma unroll
@@ -313,30 +313,34 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
           }
         };
         bf16x8 pf[2];
-        if constexpr (C::PAIR) {
-          // The weights are handed over as they come with the pair's present reference, and formed again only
-          // where a maximum rose past it: one barrier a tile.
-          const float mx = scores(wd, 0);
-          const bool over = mx > m + 8.f;
+        if constexpr (C::WD > 1) {
+          // Wavefronts 0 and 1 of the rows form the scores of the tile's halves (2 and 3, where there are, the same
+          // again) and hand the weights over.  The weights come with the rows' present reference, and again only
+          // where a maximum rose past it: one barrier.
+          const int sub = wd & 1;
+          auto hand = [&] {
+            if (wd < 2) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) handed[wq][sub][k][lane] = __builtin_bit_cast(u32x4, pf[k]);
+            }
+          };
+          const float mx = scores(sub, 0);
           float sum = weights(s, pf);
-          rise[wd][32 * wq + l32] = over ? mx : -FLT_MAX;
-          handed[wave][0][lane] = __builtin_bit_cast(u32x4, pf[0]);
-          handed[wave][1][lane] = __builtin_bit_cast(u32x4, pf[1]);
+          if (wd < 2) rise[sub][32 * wq + l32] = mx > m + 8.f ? mx : -FLT_MAX;
+          hand();
           lds_barrier();
           const int r = lane % C::kRows;
           if (__any(fmaxf(rise[0][r], rise[1][r]) > -FLT_MAX)) {  // the same for all wavefronts
             refer(fmaxf(rise[0][32 * wq + l32], rise[1][32 * wq + l32]));
             sum = weights(s, pf);
-            handed[wave][0][lane] = __builtin_bit_cast(u32x4, pf[0]);
-            handed[wave][1][lane] = __builtin_bit_cast(u32x4, pf[1]);
+            hand();
             lds_barrier();
           }
           l += sum;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) values(wd, k, pf[k]);
+          for (int k = 0; k < 2; ++k) values(sub, k, pf[k]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            values(wd ^ 1, k, __builtin_bit_cast(bf16x8, handed[wq + WQ * (wd ^ 1)][k][lane]));
+          for (int k = 0; k < 2; ++k) values(sub ^ 1, k, __builtin_bit_cast(bf16x8, handed[wq][sub ^ 1][k][lane]));
         } else {
 #pragma unroll 1
           for (int sub = 0; sub < 2; ++sub) {
@@ -350,14 +354,14 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
       }
     }
     l = halves_sum(l);
-    if constexpr (C::PAIR) {
+    if constexpr (C::WD > 1) {
       lds_barrier();  // the run before has read its sums
-      sums[wd][32 * wq + l32] = l;
+      if (wd < 2) sums[wd][32 * wq + l32] = l;
       lds_barrier();
       l = sums[0][32 * wq + l32] + sums[1][32 * wq + l32];
     }
     if (on) {
-      const int ch = (C::PAIR ? wd * (R / 2) : 0) + 4 * half;
+      const int ch = wd * (32 * C::kOut) + 4 * half;
       const bool first = half == 0 && wd == 0;
       if (whole) {
         const float r = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees nothing
