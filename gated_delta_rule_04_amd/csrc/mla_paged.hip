@@ -178,7 +178,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
     const int stop = min(t1, seen < 0 ? 0 : seen / kTile + 1);
     const int m0 = block * C::kRows + 32 * wq, mi = m0 + l32;
     const bool on = mi < rows;
-    const int lim = on ? sq.L - sq.Lq + mi / a.H : INT_MAX;  // a row that is not one: zero queries, not written
+    const int lim = on ? sq.L - sq.Lq + mi / a.H : INT_MAX;
     const long long row = (long long)sq.first * a.H + mi;
     const int* table = a.table + (long long)n * a.max_pages;
 
@@ -214,13 +214,18 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
     f32x16 acc[C::kOut] = {};
     float m = -FLT_MAX, l = 0.f;
     if (t0 < stop) {
+      // A row that is not one reads the last again, and is not written.  (With 256 registers of sums, loads a branch
+      // each keep the register allocator from spilling.)
+      constexpr bool kMost = R < 512 || C::WD > 1;
+      const bf16* q_row = a.q + ((long long)sq.first * a.H + min(mi, rows - 1)) * D;
       bf16x8 qf[D / 16];
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) qf[s] = on ? row_frag(a.q + row * D, s, half) : bf16x8{};
+      for (int s = 0; s < D / 16; ++s) qf[s] = kMost || on ? row_frag(q_row, s, half) : bf16x8{};
       int p0 = t0;
       __syncthreads();  // the run before is done with the buffers
       look_up(p0);
       __syncthreads();
+      if constexpr (kMost) arrived(qf);
       int mine = places[lane];
 #pragma unroll
       for (int i = 0; i < C::kLatLoads; ++i) fetch_lat(i, max(mine, 0), 0, ~0ull);

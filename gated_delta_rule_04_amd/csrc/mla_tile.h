@@ -123,6 +123,14 @@ __device__ __forceinline__ void tile_barrier() {
 }
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Waits for operands loaded into registers, here and not inside the loop that
+// uses them, where the wait would be for the tiles on their way too.
+template <int N>
+__device__ __forceinline__ void arrived(bf16x8 (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i]));
+}
+
 // Rows 0 .. ROWS-1 of W channels from a strided tensor into a tile, by 4
 // wavefronts; rows after `last` read it again (their weights are zero).
 template <int ROWS, int W>

@@ -15,25 +15,16 @@ k_pe [B, T, Dr] shared by the heads (None: Dr = 0); o [B, T, H, Dv].  bfloat16;
 lse float32.  Calls run on the current stream of the tensors' device.
 """
 
-import contextlib
-import ctypes
+import functools
 import math
 
 import torch
 
-from .kda import KDA_BF16, KDA_F16, KDA_F32, KdaError, _check_dev, _expect, _num_seqs, _ptr, lib
+from .kda import KDA_BF16, KDA_F16, KDA_F32, KdaError, _num_seqs, lib
 
 __all__ = ["cache_append", "paged_attn", "paged_workspace_bytes", "attn_fwd", "attn_bwd", "attn_bwd_workspace_bytes"]
 
 _DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.float16: KDA_F16}
-
-
-def _same(first, *ts, dtype=None, name):
-    """Raise unless every given tensor has `dtype` (first's dtype by default)."""
-    want = first.dtype if dtype is None else dtype
-    for t in ts:
-        if t is not None and t.dtype != want:
-            raise TypeError("%s must be %s" % (name, str(want).replace("torch.", "")))
 
 
 def _dt(t):
@@ -42,23 +33,54 @@ def _dt(t):
     return _DT[t.dtype]
 
 
-def _check(*ts):
-    """Contiguous GPU tensors of one device."""
-    _check_dev(*ts)
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError("tensors must be on one device, got %s" % sorted(str(d) for d in devs))
+def _check(first, *tensors):
+    """Each of (tensor or None, name, shape, dtype) as said, contiguous and on
+    `first`'s device, which is a GPU: the kernels size every access from the
+    first tensors' sizes.  A shape of None is not compared."""
+    for t, name, shape, dtype in tensors:
+        if t is None:
+            continue
+        if shape is not None and t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
+    dev = first.device
+    if not first.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if not first.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    for t, name, _, _ in tensors:
+        if t is not None:
+            if t.device != dev:
+                raise ValueError("tensors must be on one device: %s is on %s" % (name, t.device))
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous: %s" % name)
+    return dev
 
 
-@contextlib.contextmanager
-def _on(t):
-    """t's device made current; yields its current stream."""
-    with torch.cuda.device(t.device):
-        yield ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _nbytes(ws):
-    return 0 if ws is None else ws.numel() * ws.element_size()
+def _call(name, dev, *args):
+    """Library call `name` on dev's current stream, with dev current."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise KdaError(st, name)
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace (any contiguous tensor of dev), or one of `need` bytes; with its size."""
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the tensors' device")
+        return workspace, workspace.numel() * workspace.element_size()
+    return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
 
 
 def cache_append(c_kv, positions, slots, cache, latent_dim, rope=None, norm_weight=None, eps=1e-6, interleaved=False,
@@ -75,39 +97,30 @@ def cache_append(c_kv, positions, slots, cache, latent_dim, rope=None, norm_weig
     T, D = c_kv.shape
     R = int(latent_dim)
     Dr = D - R
-    _expect(cache, (cache.shape[0], cache.shape[1], D), "cache")
-    _expect(slots, (T,), "slots")
-    _expect(positions, (T,), "positions")
-    _expect(norm_weight, (R,), "norm_weight")
+    H = 1
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs positions")
         if rope.dim() != 2:
             raise ValueError("rope must be [num_pos, Dr]")
-        _expect(rope, (rope.shape[0], Dr), "rope")
     if (q_pe is None) != (q is None):
         raise ValueError("q_pe and q go together")
-    H = 1
     if q_pe is not None:
         if q_pe.dim() != 3:
             raise ValueError("q_pe must be [T, H, Dr]")
         H = q_pe.shape[1]
-        _expect(q_pe, (T, H, Dr), "q_pe")
-        _expect(q, (T, H, D), "q")
-    _same(c_kv, cache, q_pe, q, name="cache, q_pe and q (c_kv's dtype)")
-    _same(c_kv, norm_weight, rope, dtype=torch.float32, name="norm_weight and rope")
-    _same(c_kv, positions, slots, dtype=torch.int32, name="positions and slots")
-    _check(c_kv, positions, slots, cache, rope, norm_weight, q_pe, q)
-    with _on(c_kv) as stream:
-        st = lib().kda_mla_cache_append(_ptr(c_kv), _ptr(norm_weight), float(eps), _ptr(rope),
-                                        0 if rope is None else rope.shape[0], int(bool(interleaved)),
-                                        _ptr(positions), _ptr(slots), _ptr(cache), cache.shape[0], cache.shape[1],
-                                        _ptr(q_pe), _ptr(q), T, H, R, Dr, _dt(c_kv), stream)
-    if st != 0:
-        raise KdaError(st, "kda_mla_cache_append")
+    dt, f32, i32 = c_kv.dtype, torch.float32, torch.int32
+    dev = _check(c_kv, (cache, "cache", (cache.shape[0], cache.shape[1], D), dt), (slots, "slots", (T,), i32),
+                 (positions, "positions", (T,), i32), (norm_weight, "norm_weight", (R,), f32),
+                 (rope, "rope", None if rope is None else (rope.shape[0], Dr), f32), (q_pe, "q_pe", (T, H, Dr), dt),
+                 (q, "q", (T, H, D), dt))
+    _call("kda_mla_cache_append", dev, _ptr(c_kv), _ptr(norm_weight), float(eps), _ptr(rope),
+          0 if rope is None else rope.shape[0], int(bool(interleaved)), _ptr(positions), _ptr(slots), _ptr(cache),
+          cache.shape[0], cache.shape[1], _ptr(q_pe), _ptr(q), T, H, R, Dr, _dt(c_kv))
     return cache
 
 
+@functools.lru_cache(maxsize=256)
 def paged_workspace_bytes(N, Tq, H, R, Dr, page_size, max_pages, dtype=torch.bfloat16):
     """Bytes of device workspace paged_attn needs."""
     return int(lib().kda_mla_paged_workspace_bytes(N, Tq, H, R, Dr, page_size, max_pages, _DT[dtype]))
@@ -125,33 +138,25 @@ def paged_attn(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=No
     N, max_pages = block_table.shape
     num_pages, page_size, _ = cache.shape
     R = int(latent_dim)
-    _expect(cache, (num_pages, page_size, D), "cache")
-    _expect(seq_lens, (N,), "seq_lens")
-    if cu_seqlens is None:
-        _expect(q, (N, H, D), "q (one token a sequence)")
-    else:
-        _expect(cu_seqlens, (N + 1,), "cu_seqlens")
-    _expect(out, (Tq, H, R), "out")
-    _expect(lse, (Tq, H), "lse")
-    _same(q, cache, out, name="cache and out (q's dtype)")
-    _same(q, block_table, seq_lens, cu_seqlens, dtype=torch.int32, name="block_table, seq_lens and cu_seqlens")
-    _same(q, lse, dtype=torch.float32, name="lse")
-    dt = _dt(q)
-    _check(q, cache, block_table, seq_lens, cu_seqlens, out, lse, workspace)
-    with _on(q) as stream:
-        o = out if out is not None else torch.empty((Tq, H, max(R, 0)), dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-        ws = workspace
-        if ws is None:
-            need = paged_workspace_bytes(N, Tq, H, R, D - R, page_size, max_pages, q.dtype)
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        st = lib().kda_mla_paged_attn(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens),
-                                      _ptr(o), _ptr(lse), N, Tq, H, R, D - R, num_pages, page_size, max_pages,
-                                      float(scale), dt, _ptr(ws), _nbytes(ws), stream)
-    if st != 0:
-        raise KdaError(st, "kda_mla_paged_attn")
-    return o, lse
+    if cu_seqlens is None and N != Tq:
+        raise ValueError("q must be [N, H, R + Dr], one token a sequence, without cu_seqlens")
+    dt, i32 = q.dtype, torch.int32
+    dev = _check(q, (cache, "cache", (num_pages, page_size, D), dt), (block_table, "block_table", None, i32),
+                 (seq_lens, "seq_lens", (N,), i32), (cu_seqlens, "cu_seqlens", (N + 1,), i32),
+                 (out, "out", (Tq, H, R), dt), (lse, "lse", (Tq, H), torch.float32))
+    code = _dt(q)
+    if not 0 <= R <= D:
+        raise ValueError("latent_dim must be within q's width")
+    if out is None:
+        out = torch.empty((Tq, H, R), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+    ws, nbytes = _workspace(workspace, 0 if workspace is not None else
+                            paged_workspace_bytes(N, Tq, H, R, D - R, page_size, max_pages, dt), dev)
+    _call("kda_mla_paged_attn", dev, _ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens),
+          _ptr(out), _ptr(lse), N, Tq, H, R, D - R, num_pages, page_size, max_pages, float(scale), code, _ptr(ws),
+          nbytes)
+    return out, lse
 
 
 def _expanded_shapes(q, kv, k_pe):
@@ -164,9 +169,7 @@ def _expanded_shapes(q, kv, k_pe):
         if k_pe.dim() != 3:
             raise ValueError("k_pe must be [B, T, Dr]")
         Dr = k_pe.shape[-1]
-        _expect(k_pe, (B, T, Dr), "k_pe")
     Dn = Dq - Dr
-    _expect(kv, (B, T, H, kv.shape[-1]), "kv")
     Dv = kv.shape[-1] - Dn
     if Dn <= 0 or Dv <= 0:
         raise ValueError("q, kv and k_pe widths do not fit: q [.., Dn + Dr], kv [.., Dn + Dv], k_pe [.., Dr]")
@@ -178,24 +181,21 @@ def attn_fwd(q, kv, k_pe=None, scale=None, cu_seqlens=None, out=None, lse=None):
     Returns (o [B, T, H, Dv], lse [B, T, H])."""
     B, T, H, Dn, Dr, Dv = _expanded_shapes(q, kv, k_pe)
     N = _num_seqs(B, cu_seqlens)
-    _expect(out, (B, T, H, Dv), "out")
-    _expect(lse, (B, T, H), "lse")
-    _same(q, kv, k_pe, out, name="kv, k_pe and out (q's dtype)")
-    _same(q, lse, dtype=torch.float32, name="lse")
-    dt = _dt(q)
-    _check(q, kv, k_pe, cu_seqlens, out, lse)
-    scale = 1.0 / math.sqrt(Dn + Dr) if scale is None else float(scale)
-    with _on(q) as stream:
-        o = out if out is not None else torch.empty((B, T, H, Dv), dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
-        st = lib().kda_mla_attn_fwd(_ptr(q), _ptr(kv), _ptr(k_pe), _ptr(o), _ptr(lse), _ptr(cu_seqlens), N, B, T, H,
-                                    Dn, Dr, Dv, scale, dt, stream)
-    if st != 0:
-        raise KdaError(st, "kda_mla_attn_fwd")
-    return o, lse
+    dt = q.dtype
+    dev = _check(q, (kv, "kv", (B, T, H, Dn + Dv), dt), (k_pe, "k_pe", (B, T, Dr), dt),
+                 (cu_seqlens, "cu_seqlens", None, torch.int32), (out, "out", (B, T, H, Dv), dt),
+                 (lse, "lse", (B, T, H), torch.float32))
+    code = _dt(q)
+    if out is None:
+        out = torch.empty((B, T, H, Dv), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    _call("kda_mla_attn_fwd", dev, _ptr(q), _ptr(kv), _ptr(k_pe), _ptr(out), _ptr(lse), _ptr(cu_seqlens), N, B, T, H,
+          Dn, Dr, Dv, 1.0 / math.sqrt(Dn + Dr) if scale is None else float(scale), code)
+    return out, lse
 
 
+@functools.lru_cache(maxsize=256)
 def attn_bwd_workspace_bytes(B, T, H, Dn, Dr, Dv, num_seqs, dtype=torch.bfloat16):
     """Bytes of device workspace attn_bwd needs."""
     return int(lib().kda_mla_attn_bwd_workspace_bytes(B, T, H, Dn, Dr, Dv, num_seqs, _DT[dtype]))
@@ -207,30 +207,19 @@ def attn_bwd(q, kv, k_pe, o, lse, do, scale=None, cu_seqlens=None, workspace=Non
     without k_pe); `out` takes preallocated ones."""
     B, T, H, Dn, Dr, Dv = _expanded_shapes(q, kv, k_pe)
     N = _num_seqs(B, cu_seqlens)
-    _expect(o, (B, T, H, Dv), "o")
-    _expect(do, (B, T, H, Dv), "do")
-    _expect(lse, (B, T, H), "lse")
-    _same(q, kv, k_pe, o, do, name="kv, k_pe, o and do (q's dtype)")
-    _same(q, lse, dtype=torch.float32, name="lse")
-    dt = _dt(q)
-    _check(q, kv, k_pe, o, lse, do, cu_seqlens, workspace)
-    scale = 1.0 / math.sqrt(Dn + Dr) if scale is None else float(scale)
-    shapes = {"dq": (B, T, H, Dn + Dr), "dkv": (B, T, H, Dn + Dv), "dk_pe": (B, T, Dr) if Dr else None}
-    with _on(q) as stream:
-        gr = {}
-        for n, shape in shapes.items():
-            t = None if out is None or shape is None else out.get(n)
-            _expect(t, shape, n)
-            _same(q, t, name=n)
-            gr[n] = t if t is not None or shape is None else torch.empty(shape, dtype=q.dtype, device=q.device)
-        _check(q, *gr.values())
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(max(attn_bwd_workspace_bytes(B, T, H, Dn, Dr, Dv, N, q.dtype), 1), dtype=torch.uint8,
-                             device=q.device)
-        st = lib().kda_mla_attn_bwd(_ptr(q), _ptr(kv), _ptr(k_pe), _ptr(o), _ptr(lse), _ptr(do), _ptr(gr["dq"]),
-                                    _ptr(gr["dkv"]), _ptr(gr["dk_pe"]), _ptr(cu_seqlens), N, B, T, H, Dn, Dr, Dv,
-                                    scale, dt, _ptr(ws), _nbytes(ws), stream)
-    if st != 0:
-        raise KdaError(st, "kda_mla_attn_bwd")
+    dt = q.dtype
+    shapes = {"dq": (B, T, H, Dn + Dr), "dkv": (B, T, H, Dn + Dv), "dk_pe": (B, T, Dr)}
+    gr = {n: None if out is None else out.get(n) for n in shapes}
+    dev = _check(q, (kv, "kv", (B, T, H, Dn + Dv), dt), (k_pe, "k_pe", (B, T, Dr), dt), (o, "o", (B, T, H, Dv), dt),
+                 (do, "do", (B, T, H, Dv), dt), (lse, "lse", (B, T, H), torch.float32),
+                 (cu_seqlens, "cu_seqlens", None, torch.int32), *((gr[n], n, shapes[n], dt) for n in gr))
+    code = _dt(q)
+    for n in gr:
+        if gr[n] is None and (n != "dk_pe" or Dr):
+            gr[n] = torch.empty(shapes[n], dtype=dt, device=dev)
+    ws, nbytes = _workspace(workspace, 0 if workspace is not None else
+                            attn_bwd_workspace_bytes(B, T, H, Dn, Dr, Dv, N, dt), dev)
+    _call("kda_mla_attn_bwd", dev, _ptr(q), _ptr(kv), _ptr(k_pe), _ptr(o), _ptr(lse), _ptr(do), _ptr(gr["dq"]),
+          _ptr(gr["dkv"]), _ptr(gr["dk_pe"]), _ptr(cu_seqlens), N, B, T, H, Dn, Dr, Dv,
+          1.0 / math.sqrt(Dn + Dr) if scale is None else float(scale), code, _ptr(ws), nbytes)
     return gr
