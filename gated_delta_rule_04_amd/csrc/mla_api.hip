@@ -13,6 +13,12 @@ namespace {
 
 constexpr int kMaxHeads = 1024;     // a 128-token span of one tensor stays below 2 GiB
 constexpr int kMaxPagedSeqs = 65536;
+// A launch counts its threads in 32 bits, and workgroups have 256: tiles of 128
+// tokens of every document and head, 4 rows a workgroup of the paged form's
+// join, 16 threads a token for dk_pe.
+constexpr int kMaxBlocks = (1 << 24) - 1;
+constexpr int kMaxPagedRows = (1 << 26) - 256;
+constexpr int kMaxTokens = 1 << 27;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -39,9 +45,8 @@ kda_status check_attn(const int* cu, int num_seqs, int B, int T, int H, int Dn, 
   if (B < 0 || T < 0 || H <= 0 || H > kMaxHeads || num_seqs < 0 || !scale_ok(scale)) return KDA_ERR_SHAPE;
   if (!heads_ok(Dn, Dr, Dv)) return KDA_ERR_UNSUPPORTED;
   if (cu ? B != 1 : num_seqs != B) return KDA_ERR_SHAPE;
-  // tokens, and the launch grid of 64-token tiles of every document and head
   const long long tokens = (long long)B * T;
-  if (tokens > INT_MAX - 256 || (tokens / 64 + num_seqs + 1) * H > INT_MAX) return KDA_ERR_SHAPE;
+  if (tokens > kMaxTokens || (tokens / 128 + num_seqs + 1) * H > kMaxBlocks) return KDA_ERR_SHAPE;
   return KDA_OK;
 }
 
@@ -65,9 +70,10 @@ kda_status kda_mla_cache_append(const void* c_kv, const float* norm_weight, floa
                                 int num_pages, int page_size, const void* q_pe, void* q, int T, int H, int R, int Dr,
                                 kda_dtype dt, void* stream) {
   if (const kda_status s = check_type(dt)) return s;
-  if (T < 0 || T > INT_MAX - 256 || num_pages < 0 || page_size < 1 || !(eps >= 0.f)) return KDA_ERR_SHAPE;
+  if (T < 0 || T > kMaxTokens || num_pages < 0 || page_size < 1 || !(eps >= 0.f)) return KDA_ERR_SHAPE;
   if ((long long)num_pages * page_size > INT_MAX) return KDA_ERR_SHAPE;
   if (q_pe && (H <= 0 || H > kMaxHeads)) return KDA_ERR_SHAPE;
+  if (((long long)T * (64 + 4 * (1 + (q_pe ? H : 0)))) / 256 + 2 > kMaxBlocks) return KDA_ERR_SHAPE;
   if (rope && num_pos < 1) return KDA_ERR_SHAPE;
   if (!latent_ok(R, Dr) || (Dr == 0 && (q_pe || rope))) return KDA_ERR_UNSUPPORTED;
   if (T == 0) return KDA_OK;
@@ -93,7 +99,7 @@ kda_status kda_mla_cache_append(const void* c_kv, const float* norm_weight, floa
 
 static bool paged_sizes_ok(int N, int Tq, int H, int R, int Dr, int page_size, int max_pages) {
   return N >= 0 && N <= kMaxPagedSeqs && Tq >= 0 && H > 0 && H <= kMaxHeads && page_size >= 1 && max_pages >= 0 &&
-         (long long)page_size * max_pages <= INT_MAX - 256 && (long long)Tq * H <= INT_MAX - 256;
+         (long long)page_size * max_pages <= INT_MAX - 256 && (long long)Tq * H <= kMaxPagedRows;
 }
 
 size_t kda_mla_paged_workspace_bytes(int N, int Tq, int H, int R, int Dr, int page_size, int max_pages,

@@ -112,7 +112,6 @@ hipError_t launch(const AppendArgs& a, hipStream_t stream) {
   const int latent = (a.T + kRows - 1) / kRows;
   const long long units = DR ? (long long)a.T * (a.H + 1) * (DR / 16) : 0;
   const long long blocks = latent + (units + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   append_kernel<R, DR><<<dim3((unsigned)blocks), dim3(kThreads), 0, stream>>>(a, latent);
   return hipGetLastError();
 }

@@ -426,7 +426,9 @@ kda_status kda_short_conv_step(const void* x, const void* weight, void* conv_sta
  * bf16 and float tensor 16-byte aligned, a workspace 256-byte aligned
  * (KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE).  scale must be finite and
  * positive (KDA_ERR_SHAPE).  A non-finite value may reach every row of its
- * own sequence, never another sequence's.
+ * own sequence, never another sequence's.  Outputs and workspaces must not
+ * overlap inputs or each other.  Calls that overlap in time need workspaces
+ * of their own.
  * ------------------------------------------------------------------------- */
 
 /* Prepares new tokens for the absorbed form: their cache rows, normalised and
@@ -456,7 +458,7 @@ kda_status kda_short_conv_step(const void* x, const void* weight, void* conv_sta
  *          rotated rows in its last Dr channels (for every token, kept or
  *          not); its other channels are not touched.  H is read only then.
  * Supported: R in {128, 256, 512}, Dr in {0, 64}; num_pages * page_size below
- * 2^31.  T = 0 is a no-op.  Errors: KDA_ERR_NULL (also a rope without
+ * 2^31, T at most 2^27 and T * (H + 17) below 2^30.  T = 0 is a no-op.  Errors: KDA_ERR_NULL (also a rope without
  * positions, q_pe without q), KDA_ERR_SHAPE (also eps < 0 or NaN, rope with
  * num_pos < 1), KDA_ERR_DTYPE, KDA_ERR_UNSUPPORTED (also q_pe or rope with
  * Dr = 0), KDA_ERR_HIP.
@@ -493,7 +495,8 @@ size_t kda_mla_paged_workspace_bytes(int N, int Tq, int H, int R, int Dr, int pa
  *   workspace  at least kda_mla_paged_workspace_bytes(...) bytes; scratch.
  * Cache rows past seq_lens[n] may hold anything, NaN too.  Supported: R in
  * {128, 256, 512}, Dr in {0, 64}, page_size >= 1; num_pages * page_size,
- * max_pages * page_size and Tq * H below 2^31, N at most 65536.  N = 0 or
+ * max_pages * page_size below 2^31, Tq * H below 2^26, N at most 65536
+ * (KDA_ERR_SHAPE otherwise, as for every size limit here).  N = 0 or
  * Tq = 0 is a no-op.  Errors as elsewhere.
  */
 kda_status kda_mla_paged_attn(const void* q, const void* cache, const int* block_table, const int* seq_lens,
@@ -511,7 +514,8 @@ kda_status kda_mla_paged_attn(const void* q, const void* cache, const int* block
  *   o      [B, T, H, Dv] dt;   lse [B, T, H] f32 or NULL (kept for the backward)
  *   cu_seqlens, num_seqs, B, T: as for kda_chunk_fwd, but cu[N] may be below
  *          T: tokens from cu[N] on are padding, their outputs left as they were.
- * Supported: Dn = Dv in {64, 128}, Dr in {0, 64}.  Errors as for
+ * Supported: Dn = Dv in {64, 128}, Dr in {0, 64}; B * T at most 2^27, and
+ * (B * T / 128 + num_seqs + 1) * H below 2^24.  Errors as for
  * kda_chunk_fwd; no workspace.
  */
 kda_status kda_mla_attn_fwd(const void* q, const void* kv, const void* k_pe, void* o, float* lse,

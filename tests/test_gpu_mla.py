@@ -116,6 +116,10 @@ def test_expanded_odd_heads_and_batch():
     _check_expanded("H13 B5", *_expanded(22, 5, 70, 13, 64, 0))
 
 
+def test_expanded_most_heads():
+    _check_expanded("H 1024", *_expanded(24, 1, 40, 1024, 64, 0))
+
+
 def test_expanded_other_documents_do_not_matter():
     cu, T = [0, 90, 170, 300], 300
     q, kv, pe, do = _expanded(31, 1, T, 2, 128, 64)
@@ -258,6 +262,46 @@ def test_paged_rows_of_other_sequences_do_not_matter():
     keep = torch.tensor([0, 2], device="cuda")
     assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
     assert bool(torch.isnan(o2[1].float()).all())
+
+
+def test_paged_many_sequences():
+    """More sequences than threads of a workgroup: single tokens, and chunks with empty ones among them."""
+    r = np.random.default_rng(23)
+    lens = r.integers(0, 90, 700).tolist()
+    _check_paged("700 single", *_paged(23, lens, 16, 2, 128, 64), 128)
+    _check_paged("700 chunks", *_paged(24, lens, 16, 2, 128, 0, q_lens=r.integers(0, 4, 700).tolist(), pad=3), 128)
+
+
+def test_paged_most_heads():
+    _check_paged("H 1024", *_paged(25, [130], 64, 1024, 256, 0), 256)
+
+
+def test_paged_no_pages_and_no_rows():
+    q = _randn(26, 3, 4, 192).cuda()
+    empty = torch.empty((0, 16, 192), dtype=BF16, device="cuda")
+    for per in (0, 2):  # a table that names pages of an empty cache, and none
+        table = torch.zeros((3, per), dtype=torch.int32, device="cuda")
+        o, lse = mla.paged_attn(q, empty, table, _i32([0, 5, 9]).cuda(), 128, 0.1)
+        assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    o, lse = mla.paged_attn(q[:0], empty, table[:0], _i32([]).cuda(), 128, 0.1)
+    assert o.shape == (0, 4, 128)
+
+
+def test_two_calls_at_once_on_two_streams():
+    args = []
+    for i in range(2):
+        q, cache, table, lens, cu = _paged(27 + i, [3000, 500], 64, 12, 512, 64)
+        args.append(_cuda(q, cache, _i32(table), _i32(lens)))
+    want = [mla.paged_attn(*a, 512, 0.07) for a in args]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in args], []
+    for _ in range(3):
+        for s, a in zip(streams, args):
+            with torch.cuda.stream(s):
+                got.append(mla.paged_attn(*a, 512, 0.07))
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
 
 
 def test_paged_offsets_past_32_bits():

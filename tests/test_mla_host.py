@@ -35,6 +35,7 @@ def test_append_validation():
         assert call(**{miss: None}) == NULL, miss
     for odd in ("c", "w", "rope", "cache", "q_pe", "q"):
         assert call(**{odd: ODD}) == UNSUPPORTED, odd
+    assert call(T=(1 << 27) + 1) == SHAPE and call(T=1 << 27, H=64) == SHAPE     # threads of a launch fit 32 bits
     assert call(T=0, c=None, slots=None, cache=None) == OK
 
 
@@ -55,7 +56,7 @@ def test_paged_validation():
     assert paged(Tq=3) == SHAPE                              # one token a sequence without cu_seqlens
     assert paged(N=65537, Tq=65537) == SHAPE
     assert paged(pages=1 << 20, page=1 << 12) == SHAPE and paged(per=1 << 20, page=1 << 12) == SHAPE
-    assert paged(Tq=1 << 30, H=4, cu=P) == SHAPE
+    assert paged(Tq=1 << 24, H=4, cu=P) == SHAPE
     for scale in (0.0, -1.0, float("inf"), float("nan")):
         assert paged(scale=scale) == SHAPE
     for R, Dr in ((64, 64), (512, 32), (384, 0)):
@@ -91,6 +92,7 @@ def test_expanded_validation(fn):
     assert call(B=-1) == SHAPE and call(T=-1) == SHAPE and call(H=0) == SHAPE and call(H=1025) == SHAPE
     assert call(N=1) == SHAPE and call(cu=P) == SHAPE        # without documents N = B; with them B = 1
     assert call(B=1 << 16, N=1 << 16, T=1 << 16) == SHAPE
+    assert call(B=1, N=1 << 23, cu=P) == SHAPE and call(B=1, N=1, T=1 << 27, H=64) == SHAPE
     for scale in (0.0, -1.0, float("inf"), float("nan")):
         assert call(scale=scale) == SHAPE
     for Dn, Dr, Dv in ((96, 0, 96), (128, 32, 128), (128, 64, 64)):
