@@ -8,6 +8,10 @@
 // again (7 products in all where one pass has 5; a pass over both would add
 // dq in an order that changes from run to run, or keep it in a workspace of
 // float32 tiles).  p and ds are rounded to bf16 as operands; sums are float32.
+// B1 T16384 H12 128/64: dq 1.48 ms (matrix units 60% busy, two workgroups a CU),
+// dk and dv 2.2 ms (39%: the sums and operands of 32 keys are 320 registers, so
+// one wavefront a SIMD; 2.6 ms before the next tile's scores were formed beside
+// the weights), dk_pe's sum 9 us.
 
 #include <math.h>
 

@@ -18,6 +18,11 @@
 // the next one on its way during a tile, 16-byte pieces permuted within a row
 // so that both the row reads and the transposing reads spread over the banks.
 
+// N256 H8 R256 rows to 2,048: 44 us (4.0 TB/s, a copy moving 5.1); N64 H96
+// R512+64 to 8,192: 149 us; 4 chunks of up to 512 tokens at H96: 2.7 ms (840
+// TFLOP/s).  Bound by memory for few heads; with 128 rows a block by the
+// products and the softmax of one wavefront a SIMD in turn.
+
 #include <limits.h>
 #include <math.h>
 
@@ -36,10 +41,12 @@ struct PagedPlan {
   size_t ml, o, total;  // workspace: unit prefix of the sequences at 0, (maximum, sum) rows, partial sums
 };
 
-// Block height by the rows a sequence has: 32 rows keep 1 wavefront pair busy,
-// 128 rows read each tile once for all heads of up to 128.  Workgroups: as many
-// as run at once (LDS: one a CU at R = 512 and 256, two at 128), or the units
-// there can be.
+// Block height by the rows a sequence has, the smallest that holds them or 128:
+// a low block leaves fewer rows of its products empty (N64 R512+64 to 8,192:
+// H12 in blocks of 32 144 us, H64 in blocks of 64 155 us), a high one reads each
+// tile once for more rows (H96 in one block of 128 225 us, in two of 64 243 us;
+// chunks of 512 tokens 4.1 and 4.6 ms).  Workgroups: as many as run at once (by
+// their LDS one a CU at R = 512 and 256, two at 128), or the units there can be.
 PagedPlan paged_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   PagedPlan p;
   const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
@@ -475,7 +482,8 @@ hipError_t launch(const PagedWork& w, const PagedPlan& p, hipStream_t stream) {
   paged_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w);
   if (p.groups > 1) {
     const long long rows = (long long)w.a.Tq * w.a.H;
-    // parts a block can have: with more than 8 a row takes several workgroups
+    // Parts a block can have: with more than 8 a row takes several workgroups (8 rows of 15 parts: 4.2 us, with a
+    // wavefront a row 9.7 us; 6,144 rows of about 5 parts: 38 us, with a wavefront a row 13.5 us).
     if (p.groups > 8 * (rows / C::kRows + 1))
       combine_kernel<R, C::kRows, true><<<dim3((unsigned)(rows * (R / 128))), dim3(256), 0, stream>>>(w, p.groups);
     else

@@ -27,6 +27,11 @@ __all__ = ["cache_append", "paged_attn", "paged_workspace_bytes", "attn_fwd", "a
 _DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.float16: KDA_F16}
 
 
+def _raw_stream(index):
+    """torch.cuda.current_stream(index).cuda_stream, without making a Stream object (2 us of a 10 us call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _dt(t):
     if t.dtype not in _DT:
         raise TypeError("unsupported dtype %s (bfloat16)" % t.dtype)
@@ -66,10 +71,10 @@ def _call(name, dev, *args):
     """Library call `name` on dev's current stream, with dev current."""
     fn = getattr(lib(), name)
     if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(dev.index))
     if st != 0:
         raise KdaError(st, name)
 
@@ -148,7 +153,7 @@ def paged_attn(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=No
     if not 0 <= R <= D:
         raise ValueError("latent_dim must be within q's width")
     if out is None:
-        out = torch.empty((Tq, H, R), dtype=dt, device=dev)
+        out = q.new_empty((Tq, H, R))
     if lse is None:
         lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, 0 if workspace is not None else
@@ -187,7 +192,7 @@ def attn_fwd(q, kv, k_pe=None, scale=None, cu_seqlens=None, out=None, lse=None):
                  (lse, "lse", (B, T, H), torch.float32))
     code = _dt(q)
     if out is None:
-        out = torch.empty((B, T, H, Dv), dtype=dt, device=dev)
+        out = q.new_empty((B, T, H, Dv))
     if lse is None:
         lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
     _call("kda_mla_attn_fwd", dev, _ptr(q), _ptr(kv), _ptr(k_pe), _ptr(out), _ptr(lse), _ptr(cu_seqlens), N, B, T, H,
@@ -216,7 +221,7 @@ def attn_bwd(q, kv, k_pe, o, lse, do, scale=None, cu_seqlens=None, workspace=Non
     code = _dt(q)
     for n in gr:
         if gr[n] is None and (n != "dk_pe" or Dr):
-            gr[n] = torch.empty(shapes[n], dtype=dt, device=dev)
+            gr[n] = q.new_empty(shapes[n])
     ws, nbytes = _workspace(workspace, 0 if workspace is not None else
                             attn_bwd_workspace_bytes(B, T, H, Dn, Dr, Dv, N, dt), dev)
     _call("kda_mla_attn_bwd", dev, _ptr(q), _ptr(kv), _ptr(k_pe), _ptr(o), _ptr(lse), _ptr(do), _ptr(gr["dq"]),

@@ -21,7 +21,7 @@
  *   KDA_F16 there is KDA_ERR_DTYPE); states (h0, ht, state) are float32,
  *   except a serving pool's, whose type is a knob.  bf16 is bfloat16 with
  *   round-to-nearest-even on output.
- * - Supported head sizes: Dk, Dv in {64, 128}.  g_group in {1, 64} is the
+ * - Supported head sizes of the KDA calls: Dk, Dv in {64, 128}.  g_group in {1, 64} is the
  *   number of consecutive key channels that share one log-decay value
  *   (1 = per-channel KDA decay; 64 = the "decay-g64" ablation of the
  *   Mini-K3-1H-decay-g64 card); it must divide Dk.
@@ -33,6 +33,9 @@
  *   calls from several threads are safe as long as their buffers differ.
  * - Results are bitwise deterministic run to run (no atomics).
  * - No query scaling: pre-scale q if a scale is wanted (o is linear in q).
+ * - The latent-attention calls (kda_mla_*, at the end) state their own sizes,
+ *   types and scale.  Entry points may be added without a new ABI version;
+ *   the ones there are keep their arguments and meaning within a version.
  */
 #ifndef KDA_H
 #define KDA_H
