@@ -401,18 +401,16 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   }
 }
 
-// Joins the parts of split blocks.  A row's R channels are taken by R / SLICE
-// workgroups with SLICE / 4 threads a part: a wavefront-sized slice for few
-// parts a row (4 rows a workgroup), a 128-channel slice with 8 parts at a time
-// for many.
+// Joins the parts of split blocks: a wavefront a row for few parts, or for many
+// a workgroup for 64 channels of a row, 16 parts at a time.
 template <int R, int ROWS, bool MANY>
 __global__ __launch_bounds__(256) void combine_kernel(PagedWork w, int groups) {
-  constexpr int kSlice = MANY ? 128 : R, kAcross = kSlice / 4;      // threads over the channels
+  constexpr int kSlice = MANY ? 64 : R, kAcross = kSlice / 4;      // threads over the channels
   constexpr int kLanes = MANY ? 256 : 64, kWays = MANY ? kLanes / kAcross : 1;  // threads of a row, parts at a time
   constexpr int kQuads = MANY ? 1 : R / 256 > 0 ? R / 256 : 1;      // 4-channel pieces a thread (few parts)
   const PagedArgs& a = w.a;
   const int tid = threadIdx.x;
-  const long long row = MANY ? blockIdx.x / (R / 128) : (long long)blockIdx.x * 4 + (tid >> 6);
+  const long long row = MANY ? blockIdx.x / (R / 64) : (long long)blockIdx.x * 4 + (tid >> 6);
   if (row >= (long long)a.Tq * a.H) return;
   int n = (int)(row / a.H);
   if (a.cu) {
@@ -442,9 +440,9 @@ __global__ __launch_bounds__(256) void combine_kernel(PagedWork w, int groups) {
   float l = 0.f;
   f32x4 o[kQuads] = {};
   const int way = MANY ? tid / kAcross : 0;
-  const int ch = MANY ? (blockIdx.x % (R / 128)) * 128 + (tid % kAcross) * 4 : (tid & 63) * 4;
+  const int ch = MANY ? (blockIdx.x % (R / 64)) * 64 + (tid % kAcross) * 4 : (tid & 63) * 4;
   const bool in_row = MANY || ch < R;
-#pragma unroll 4
+#pragma unroll 8
   for (int g = g0 + way; g <= g1; g += kWays) {
     const long long at = place(g);
     const float f = kda::fast_exp2(w.ml[2 * at] - m);
@@ -485,7 +483,7 @@ hipError_t launch(const PagedWork& w, const PagedPlan& p, hipStream_t stream) {
     // Parts a block can have: with more than 8 a row takes several workgroups (8 rows of 15 parts: 4.2 us, with a
     // wavefront a row 9.7 us; 6,144 rows of about 5 parts: 38 us, with a wavefront a row 13.5 us).
     if (p.groups > 8 * (rows / C::kRows + 1))
-      combine_kernel<R, C::kRows, true><<<dim3((unsigned)(rows * (R / 128))), dim3(256), 0, stream>>>(w, p.groups);
+      combine_kernel<R, C::kRows, true><<<dim3((unsigned)(rows * (R / 64))), dim3(256), 0, stream>>>(w, p.groups);
     else
       combine_kernel<R, C::kRows, false><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(w, p.groups);
   }
