@@ -89,29 +89,40 @@ __device__ __forceinline__ unsigned long long uniform(unsigned long long x) {
 
 // 16 (or 4) bytes a lane from base + off straight to lds + 16 (4) lane.  M0
 // holds the LDS address; it may not be read by the instruction after the one
-// that writes it.  The compiler's wait counts do not see these loads, nor that
-// they write LDS: tile_barrier waits for them and orders what reads it.
+// that writes it.  The base is copied by a scalar instruction in between: it
+// may come from a vector one (a lane's value made scalar), after which a memory
+// instruction would have to wait, and the compiler does not see this one.  Nor
+// do its wait counts see these loads, or that they write LDS: tile_barrier
+// waits for them and orders what reads it.
 __device__ __forceinline__ void load_lds(const void* base, unsigned off, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(lds)), "v"(off),
-               "s"(uniform((unsigned long long)base))
+  unsigned long long at;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+               : "=&s"(at)
+               : "s"(uniform(lds)), "v"(off), "s"(uniform((unsigned long long)base))
                : "m0");
 }
 __device__ __forceinline__ void load_lds4(const void* base, unsigned off, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(uniform(lds)), "v"(off),
-               "s"(uniform((unsigned long long)base))
+  unsigned long long at;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0"
+               : "=&s"(at)
+               : "s"(uniform(lds)), "v"(off), "s"(uniform((unsigned long long)base))
                : "m0");
 }
 // The same for the lanes of `on` (all lanes are active before and after), and
 // with an address a lane.
 __device__ __forceinline__ void load_lds_if(unsigned long long on, const void* base, unsigned off, unsigned lds) {
+  unsigned long long at;
   asm volatile(
-      "s_mov_b32 m0, %0\n\ts_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1" ::"s"(uniform(lds)),
-      "v"(off), "s"(uniform((unsigned long long)base)), "s"(uniform(on))
+      "s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\ts_mov_b64 exec, %4\n\tglobal_load_lds_dwordx4 %2, %0\n\t"
+      "s_mov_b64 exec, -1"
+      : "=&s"(at)
+      : "s"(uniform(lds)), "v"(off), "s"(uniform((unsigned long long)base)), "s"(uniform(on))
       : "m0");
 }
 __device__ __forceinline__ void load_lds_if(unsigned long long on, const bf16* from, unsigned lds) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\ts_mov_b64 exec, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1" ::"s"(uniform(lds)),
+      "s_mov_b32 m0, %0\n\ts_mov_b64 exec, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1" ::"s"(
+          uniform(lds)),
       "v"(from), "s"(uniform(on))
       : "m0");
 }
