@@ -133,8 +133,10 @@ __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
 // dk and dv: S = Q K^T with the wavefront's 32 keys as B operands in registers,
 // so that P and dS come as B operands over the queries; dV^T += dO^T P and
 // dK^T += Q^T dS.  The rotary part of dk is this head's share of dk_pe.
+// Up to 128 channels two wavefronts a SIMD (B4 T4096 H16 128/0: backward 1.20 ->
+// 1.15 ms); at 128 / 64 their 256 registers spill (3.8 -> 6.6 ms at T16384 H12).
 template <int DN, int DR>
-__global__ __launch_bounds__(256, 1) void dkv_kernel(AttnArgs a, TileMap map) {
+__global__ __launch_bounds__(256, DN + DR <= 128 ? 2 : 1) void dkv_kernel(AttnArgs a, TileMap map) {
   constexpr int DQ = DN + DR;
   // bytes of a tile's parts: queries, dout, the queries' rotary parts, and each wavefront's (lse, delta) rows
   constexpr unsigned kQry = kI * DN * 2, kRot = kI * DR * 2, kStat = kI * 8, kTileBytes = 2 * kQry + kRot + 4 * kStat;
