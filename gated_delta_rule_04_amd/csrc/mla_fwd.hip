@@ -9,8 +9,8 @@
 // matrix units busy during the other's softmax.
 // Sums and statistics are float32; P is rounded to bf16 as an operand, the row
 // sum is taken before that.
-// B1 T16384 H12 128/64: 0.95 ms, 1,090 TFLOP/s, a large bf16 matrix product
-// reaching 1,551; T4096 H96: 0.55 ms.  The matrix units are busy 53 to 61% of
+// B1 T16384 H12 128/64: 0.95 to 1.04 ms by GPU, 990 to 1,090 TFLOP/s, a large
+// bf16 matrix product reaching 1,551; T4096 H96: 0.55 ms.  The matrix units are busy 53 to 61% of
 // the time; the rest is the softmax's vector work.  Before the next tile's
 // scores were formed beside the weights: 1.11 ms.
 

@@ -163,7 +163,6 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   Sequence sq = sequence<C::kRows>(a, n);
   const float c = a.scale * kda::kLog2e;
   const unsigned lds_lat = lds_address(&lat[0][0]), lds_rot = lds_address(&rot[0][0]);
-
   const LaneAt<R> at_lat(lane);
   const LaneAt<64> at_rot(lane);
   LaneAt<R> at_out = at_lat;  // of the channels whose sums this wavefront holds
