@@ -183,7 +183,6 @@ kda_status kda_mla_attn_bwd(const void* q, const void* kv, const void* k_pe, con
   a.q = static_cast<const mla::bf16*>(q);
   a.kv = static_cast<const mla::bf16*>(kv);
   a.k_pe = static_cast<const mla::bf16*>(k_pe);
-  a.o_in = static_cast<const mla::bf16*>(o);
   a.lse = const_cast<float*>(lse);
   a.dout = static_cast<const mla::bf16*>(dout);
   a.dq = static_cast<mla::bf16*>(dq);

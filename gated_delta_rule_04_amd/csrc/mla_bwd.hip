@@ -3,15 +3,16 @@
 //   p = exp(s - lse), dp = do v^T, ds = p (dp - delta), delta = <do, o> = sum_j p dp
 //   dq = scale ds k, dk = scale ds^T q, dv = p^T do
 //
-// Two passes, so that no sum needs atomics: dq_kernel goes along the keys of
-// 128 queries, dkv_kernel along the queries of 128 keys.  Each forms s and dp
-// again (7 products in all where one pass has 5; a pass over both would add
-// dq in an order that changes from run to run, or keep it in a workspace of
-// float32 tiles).  p and ds are rounded to bf16 as operands; sums are float32.
-// B1 T16384 H12 128/64: dq 1.48 ms (matrix units 60% busy, two workgroups a CU),
-// dk and dv 2.2 ms (39%: the sums and operands of 32 keys are 320 registers, so
-// one wavefront a SIMD; 2.6 ms before the next tile's scores were formed beside
-// the weights), dk_pe's sum 9 us.
+// Three passes, so that no sum needs atomics: delta_kernel and dq_kernel go along
+// the keys of 128 queries, dkv_kernel along the queries of 128 keys.  Each forms
+// s and dp again (9 products in all where one pass over saved deltas has 5; a
+// pass over both directions would add dq in an order that changes from run to
+// run, or keep it in a workspace of float32 tiles).  p and ds are rounded to
+// bf16 as operands; sums are float32.
+// B1 T16384 H12 128/64: delta 0.92 ms (three workgroups a CU; tiles of 64 keys at
+// two a CU 1.07), dq 1.53 ms, dk and dv 2.2 to 2.3 ms (the sums and operands of
+// 32 keys are 339 registers, so one wavefront a SIMD; 2.6 ms before the next
+// tile's scores were formed beside the weights), dk_pe's sum 9 us.
 
 #include <math.h>
 
@@ -21,15 +22,87 @@ namespace mla {
 namespace {
 
 constexpr int kRows = 128;  // queries (or keys) of a workgroup, 32 a wavefront
-constexpr int kK = 32;      // keys of a tile of the dq kernel
+constexpr int kK = 32;      // keys of a tile of the delta and dq kernels
 constexpr int kI = 32;      // queries of a tile of the dk, dv kernel
 
-// dq.  Also writes delta for the other kernel, summed as sum_j p dp in float32
-// (the rounded o would put half a bf16 step of o into every ds).  A workgroup
-// that starts a document takes delta from a pass of its own over its 128 keys
-// first: there rows see few keys, and the rounding of o would show in dq.
-// Further rows use <do, o> of the rounded o, whose error their many keys
-// average down.
+// Tiles of kK keys of a head: keys, values and rotary keys one after another.
+template <int DN, int DR>
+struct KeyTiles {
+  static constexpr unsigned kKey = kK * DN * 2;
+  const bf16 *kv, *pe;
+  int ld, len;
+  __device__ __forceinline__ KeyTiles(const AttnArgs& a, long long t0, int h, int len)
+      : kv(a.kv + (t0 * a.H + h) * (2 * DN)), pe(a.k_pe + t0 * DR), ld(a.H * 2 * DN), len(len) {}
+  __device__ __forceinline__ void fetch(int j0, unsigned to, int wave, int lane) const {
+    const bf16* from = kv + (long long)j0 * ld;
+    fetch_rows<kK, DN>(from, ld, len - 1 - j0, to, wave, lane);
+    fetch_rows<kK, DN>(from + DN, ld, len - 1 - j0, to + kKey, wave, lane);
+    if constexpr (DR > 0) fetch_rows<kK, DR>(pe + (long long)j0 * DR, DR, len - 1 - j0, to + 2 * kKey, wave, lane);
+  }
+};
+
+// Each query's log-sum-exp in log2 units and its delta, for the two kernels
+// after it: delta = sum_j p dp in float32, along the keys of 128 queries.  The
+// rounded o would be at hand, but <do, o> carries its rounding as one term in
+// all of a row's ds; where a row attends to few keys, p (dp - delta) is small
+// beside that term, and dq mostly rounding (scores of standard deviation 8: a
+// row's dq off by 65% at the 95th percentile, by 0.3% with this sum).
+template <int DN, int DR>
+__global__ __launch_bounds__(256, 2) void delta_kernel(AttnArgs a, TileMap map) {
+  constexpr int DQ = DN + DR;
+  constexpr unsigned kKey = kK * DN * 2, kRot = kK * DR * 2;  // bytes of a tile's parts: keys, values, rotary keys
+  __shared__ __align__(1024) char lds[2][2 * kKey + kRot];
+  int h, len, q0;
+  long long t0;
+  if (!tile_place<kRows>(a, map, true, h, t0, len, q0)) return;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w0 = q0 + wave * 32;
+  const int qi = w0 + (lane & 31);
+  const int keys = min(len, q0 + kRows);
+  const long long row = (t0 + qi) * a.H + h;
+  const bool on = qi < len;
+
+  bf16x8 qf[DQ / 16], df[DN / 16];
+#pragma unroll
+  for (int s = 0; s < DQ / 16; ++s) qf[s] = on ? row_frag(a.q + row * DQ, s, half) : bf16x8{};
+#pragma unroll
+  for (int s = 0; s < DN / 16; ++s) df[s] = on ? row_frag(a.dout + row * DN, s, half) : bf16x8{};
+  const float lse = on ? a.lse[row] * kda::kLog2e : 0.f;
+  const float c = a.scale * kda::kLog2e;
+
+  const unsigned base = lds_address(&lds[0][0]);
+  const LaneAt<DN> at(lane);
+  const LaneAt<64> at_rot(lane);
+  const KeyTiles<DN, DR> tiles(a, t0, h, len);
+  float delta = 0.f;  // this lane's half of sum_j p dp
+  tiles.fetch(0, base, wave, lane);
+  for (int j0 = 0; j0 < keys; j0 += kK) {
+    const unsigned b = (j0 / kK) & 1, ks = base + b * (2 * kKey + kRot), vs = ks + kKey, rs = vs + kKey;
+    tile_barrier<0>();  // this tile is there, and all are done with the one before
+    if (j0 + kK < keys) tiles.fetch(j0 + kK, base + (b ^ 1) * (2 * kKey + kRot), wave, lane);
+    if (j0 > w0 + 31) continue;
+    f32x16 s = {}, dp = {};
+#pragma unroll
+    for (int k = 0; k < DN / 16; ++k) {
+      s = mma(row_frag(ks, at, 0, k), qf[k], s);
+      dp = mma(row_frag(vs, at, 0, k), df[k], dp);
+    }
+#pragma unroll
+    for (int k = 0; k < DR / 16; ++k) s = mma(row_frag(rs, at_rot, 0, k), qf[DN / 16 + k], s);
+    if (j0 + kK - 1 > w0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (j0 + acc_row(i, half) > qi) s[i] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      delta = __builtin_fmaf(kda::fast_exp2(__builtin_fmaf(s[i], c, -lse)), dp[i], delta);
+  }
+  delta = halves_sum(delta);
+  if (on && half == 0) *(f32x2*)(a.delta + 2 * row) = f32x2{lse, delta};
+}
+
+// dq.
 template <int DN, int DR>
 __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
   constexpr int DQ = DN + DR;
@@ -42,84 +115,55 @@ __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w0 = q0 + wave * 32;
   const int qi = w0 + (lane & 31);
   const int keys = min(len, q0 + kRows);
-  const int ld = a.H * 2 * DN;
-  const bf16* kv = a.kv + (t0 * a.H + h) * (2 * DN);
-  const bf16* pe = a.k_pe + t0 * DR;
   const long long row = (t0 + qi) * a.H + h;
   const bool on = qi < len;
 
   bf16x8 qf[DQ / 16], df[DN / 16];
-  float lse = 0.f, delta = 0.f;
 #pragma unroll
   for (int s = 0; s < DQ / 16; ++s) qf[s] = on ? row_frag(a.q + row * DQ, s, half) : bf16x8{};
 #pragma unroll
-  for (int s = 0; s < DN / 16; ++s) {
-    df[s] = on ? row_frag(a.dout + row * DN, s, half) : bf16x8{};
-    const bf16x8 of = on ? row_frag(a.o_in + row * DN, s, half) : bf16x8{};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) delta += (float)of[i] * (float)df[s][i];
-  }
-  delta = halves_sum(delta);
-  if (on) lse = a.lse[row] * kda::kLog2e;
+  for (int s = 0; s < DN / 16; ++s) df[s] = on ? row_frag(a.dout + row * DN, s, half) : bf16x8{};
+  const f32x2 stat = on ? *(const f32x2*)(a.delta + 2 * row) : f32x2{};
+  const float lse = stat[0], delta = stat[1];
   const float c = a.scale * kda::kLog2e;
 
   const unsigned base = lds_address(&lds[0][0]);
   const LaneAt<DN> at(lane);
   const LaneAt<64> at_rot(lane);
-  auto fetch = [&](int j0, int b) {
-    const unsigned to = base + b * (2 * kKey + kRot);
-    const bf16* from = kv + (long long)j0 * ld;
-    fetch_rows<kK, DN>(from, ld, len - 1 - j0, to, wave, lane);
-    fetch_rows<kK, DN>(from + DN, ld, len - 1 - j0, to + kKey, wave, lane);
-    if constexpr (DR > 0) fetch_rows<kK, DR>(pe + (long long)j0 * DR, DR, len - 1 - j0, to + 2 * kKey, wave, lane);
-  };
+  const KeyTiles<DN, DR> tiles(a, t0, h, len);
   f32x16 acc[DQ / 32] = {};
-  float sum = 0.f;  // this lane's half of sum_j p dp
-  for (int pass = q0 == 0 ? 0 : 1; pass < 2; ++pass) {
-    sum = 0.f;
-    lds_barrier();  // all are done with the pass before
-    fetch(0, 0);
-    for (int j0 = 0; j0 < keys; j0 += kK) {
-      const int b = (j0 / kK) & 1;
-      const unsigned ks = base + b * (2 * kKey + kRot), vs = ks + kKey, rs = vs + kKey;
-      tile_barrier<0>();  // this tile is there, and all are done with the one before
-      if (j0 + kK < keys) fetch(j0 + kK, b ^ 1);
-      if (j0 > w0 + 31) continue;
-      f32x16 s = {}, dp = {};
+  tiles.fetch(0, base, wave, lane);
+  for (int j0 = 0; j0 < keys; j0 += kK) {
+    const unsigned b = (j0 / kK) & 1, ks = base + b * (2 * kKey + kRot), vs = ks + kKey, rs = vs + kKey;
+    tile_barrier<0>();  // this tile is there, and all are done with the one before
+    if (j0 + kK < keys) tiles.fetch(j0 + kK, base + (b ^ 1) * (2 * kKey + kRot), wave, lane);
+    if (j0 > w0 + 31) continue;
+    f32x16 s = {}, dp = {};
 #pragma unroll
-      for (int k = 0; k < DN / 16; ++k) {
-        s = mma(row_frag(ks, at, 0, k), qf[k], s);
-        dp = mma(row_frag(vs, at, 0, k), df[k], dp);
-      }
-#pragma unroll
-      for (int k = 0; k < DR / 16; ++k) s = mma(row_frag(rs, at_rot, 0, k), qf[DN / 16 + k], s);
-      if (j0 + kK - 1 > w0) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (j0 + acc_row(i, half) > qi) s[i] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float p = kda::fast_exp2(__builtin_fmaf(s[i], c, -lse));
-        sum = __builtin_fmaf(p, dp[i], sum);
-        s[i] = p * (dp[i] - delta);
-      }
-      if (pass == 0) continue;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const bf16x8 sf = acc_frag(s, k);
-#pragma unroll
-        for (int d = 0; d < DN / 32; ++d) acc[d] = mma(tr_frag(ks, at, 16 * k, d), sf, acc[d]);
-#pragma unroll
-        for (int d = 0; d < DR / 32; ++d)
-          acc[DN / 32 + d] = mma(tr_frag(rs, at_rot, 16 * k, d), sf, acc[DN / 32 + d]);
-      }
+    for (int k = 0; k < DN / 16; ++k) {
+      s = mma(row_frag(ks, at, 0, k), qf[k], s);
+      dp = mma(row_frag(vs, at, 0, k), df[k], dp);
     }
-    sum = halves_sum(sum);
-    if (pass == 0) delta = sum;
+#pragma unroll
+    for (int k = 0; k < DR / 16; ++k) s = mma(row_frag(rs, at_rot, 0, k), qf[DN / 16 + k], s);
+    if (j0 + kK - 1 > w0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (j0 + acc_row(i, half) > qi) s[i] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = kda::fast_exp2(__builtin_fmaf(s[i], c, -lse)) * (dp[i] - delta);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bf16x8 sf = acc_frag(s, k);
+#pragma unroll
+      for (int d = 0; d < DN / 32; ++d) acc[d] = mma(tr_frag(ks, at, 16 * k, d), sf, acc[d]);
+#pragma unroll
+      for (int d = 0; d < DR / 32; ++d)
+        acc[DN / 32 + d] = mma(tr_frag(rs, at_rot, 16 * k, d), sf, acc[DN / 32 + d]);
+    }
   }
   if (!on) return;
-  if (half == 0) *(f32x2*)(a.delta + 2 * row) = f32x2{lse, sum};
 #pragma unroll
   for (int d = 0; d < DQ / 32; ++d) {
     acc[d] *= a.scale;
@@ -280,6 +324,7 @@ template <int DN, int DR>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
   const TileMap map = tile_map<kRows>(a);
   const dim3 grid((unsigned)map.blocks()), block(256);
+  delta_kernel<DN, DR><<<grid, block, 0, stream>>>(a, map);
   dq_kernel<DN, DR><<<grid, block, 0, stream>>>(a, map);
   dkv_kernel<DN, DR><<<grid, block, 0, stream>>>(a, map);
   if constexpr (DR > 0)

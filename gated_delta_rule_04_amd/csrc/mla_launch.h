@@ -49,7 +49,6 @@ struct AttnArgs {
   const bf16* q;     // [tokens][H][Dn + Dr]
   const bf16* kv;    // [tokens][H][Dn + Dv]
   const bf16* k_pe;  // [tokens][Dr]
-  const bf16* o_in;  // backward: the forward's o
   const bf16* dout;  // backward
   bf16* o;           // forward
   float* lse;        // forward: written when set; backward: read
@@ -57,7 +56,7 @@ struct AttnArgs {
   const int* cu;
   int N, T, H;       // documents; tokens of a batch row, or all of them with cu
   float scale;
-  float* delta;      // backward workspace: [tokens][H][2], lse in log2 units and <dout, o>
+  float* delta;      // backward workspace: [tokens][H][2], lse in log2 units and delta
   float* pe_part;    // backward workspace: [H][tokens][Dr]
   int tokens;
 };

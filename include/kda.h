@@ -533,7 +533,9 @@ size_t kda_mla_attn_bwd_workspace_bytes(int B, int T, int H, int Dn, int Dr, int
 /* Backward of kda_mla_attn_fwd: the gradients of L = <dout, o>.
  *
  *   q, kv, k_pe, cu_seqlens, num_seqs, sizes, scale: the forward's
- *   o, lse  the forward's outputs
+ *   o, lse  the forward's outputs.  o is not read: <dout, o> is summed again
+ *          in float32, from the weights (the rounded o would put its rounding
+ *          into every term of a row's dq, dk).
  *   dout   [B, T, H, Dv] dt
  *   dq [B, T, H, Dn + Dr] dt;  dkv [B, T, H, Dn + Dv] dt;
  *   dk_pe  [B, T, Dr] dt: summed over the heads (ignored when Dr = 0)

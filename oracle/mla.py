@@ -22,7 +22,7 @@ n u sum|.|:
     p         relative 2 ds + 64 u (exp and the row's sum, lse), and e where it
               is rounded as an operand
     o         (e + ep) sum_j p |v| + n u sum_j p |v| + e |o|
-    delta     sum_c |do| err_o (the backward reads the rounded o)
+    delta     sum_j p (ep |dp| + err_dp) + n u sum_j p |dp| (summed so in float32)
     dS        p (err_dp + err_delta) + |dS| (ep + e)
     dq, dk, dv  the operands' errors carried through the sums, + e |result|
 """
@@ -152,7 +152,7 @@ def attention_backward(q, kv, k_pe, do, scale=None, cu_seqlens=None):
             d = do[b, x, h]
             if n == 0:
                 continue
-            o, lse, err_o, err_l = attend(qq, k, v, 0, scale)
+            o, lse, _, err_l = attend(qq, k, v, 0, scale)
             ok = np.tril(np.ones((n, n), bool))
             p = np.where(ok, np.exp(np.where(ok, qq @ k.T * scale, -np.inf) - lse[:, None]), 0.0)
             dp = d @ v.T
@@ -163,10 +163,10 @@ def attention_backward(q, kv, k_pe, do, scale=None, cu_seqlens=None):
             ep = es + err_l[:, None] + 64 * U
             Dv = v.shape[1]
             e_dp = (Dv + 4) * U * (A(d) @ A(v).T)
-            e_delta = (A(d) * err_o).sum(-1, keepdims=True) + (Dv + 4) * U * (A(d) * A(o)).sum(-1, keepdims=True)
+            nU = (n + 8) * U
+            e_delta = (p * (ep * A(dp) + (1 + ep) * e_dp + nU * A(dp))).sum(-1, keepdims=True)
             e_ds = p * (e_dp + e_delta) * (1 + ep) + A(ds) * (ep + E)
             e_p = p * (ep + E)
-            nU = (n + 8) * U
             dq, dk, dv = ds @ k * scale, ds.T @ qq * scale, p.T @ d
             e_dq = (e_ds @ A(k) + nU * (A(ds) @ A(k))) * scale + E * A(dq)
             e_dk = (e_ds.T @ A(qq) + nU * (A(ds).T @ A(qq))) * scale

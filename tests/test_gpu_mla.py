@@ -111,6 +111,15 @@ def test_expanded_scales_and_large_scores(scale):
     _check_expanded("large", q, kv, pe, do, scale=scale)
 
 
+@pytest.mark.parametrize("Dn,Dr", HEADS)
+@pytest.mark.parametrize("mul", [4, 8])
+def test_expanded_rows_that_attend_to_few_keys(Dn, Dr, mul):
+    """Sharp rows far into a document: their dS is small beside any common error of delta."""
+    print("CASE sharp", Dn, Dr, mul, flush=True)
+    _check_expanded("sharp", *_expanded(61, 1, 400, 2, Dn, Dr, scale=mul))
+    _check_expanded("sharp docs", *_expanded(62, 1, 500, 1, Dn, Dr, scale=mul), cu=[0, 190, 191, 480])
+
+
 def test_expanded_odd_heads_and_batch():
     _check_expanded("H1", *_expanded(21, 1, 150, 1, 128, 64))
     _check_expanded("H13 B5", *_expanded(22, 5, 70, 13, 64, 0))

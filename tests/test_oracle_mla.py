@@ -4,6 +4,7 @@ zero nor wide."""
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import mla as orc
 
@@ -112,3 +113,34 @@ def test_rotation_keeps_norms_and_relative_angles(interleaved):
     row, _ = orc.append(c, 3, norm_weight=np.array([1.0, 2.0, 3.0]), eps=0.0)
     np.testing.assert_allclose((row[:, :3] / [1, 2, 3]) ** 2 @ np.ones(3), 3.0)
     np.testing.assert_array_equal(row[:, 3:], c[:, 3:])
+
+
+def _bf16(x):
+    return torch.tensor(np.asarray(x, np.float32)).to(torch.bfloat16).double().numpy()
+
+
+@pytest.mark.parametrize("mul", [4, 8])
+def test_bounds_tell_a_delta_of_the_rounded_output(mul):
+    """Rows that attend to few keys: the float32 sum of p dp keeps dq inside the bounds, <do, o> of the rounded o does
+    not (a planted mistake)."""
+    g = torch.Generator().manual_seed(3)
+    T, D, Dv = 400, 192, 128
+    q, k, v, do = (_bf16(torch.randn((T, n), generator=g) * c) for n, c in ((D, mul), (D, 1), (Dv, 1), (Dv, 1)))
+    kv = np.concatenate([k, v], -1)[None, :, None]
+    want, err = orc.attention_backward(q[None, :, None], kv, None, do[None, :, None])
+    want, err = want["dq"][0, :, 0], err["dq"][0, :, 0]
+    f = np.float32
+    scale = f(D ** -0.5)
+    s = np.where(np.tril(np.ones((T, T), bool)), q.astype(f) @ k.astype(f).T * scale, f(-np.inf))
+    top = s.max(-1, keepdims=True)
+    e = np.exp(s - top)
+    lse = top + np.log(e.sum(-1, keepdims=True))
+    p, dp = np.exp(s - lse), do.astype(f) @ v.astype(f).T
+    o = _bf16(_bf16(e).astype(f) @ v.astype(f) / e.sum(-1, keepdims=True))
+
+    def worst(delta):
+        ds = _bf16(p * (dp - delta)).astype(f)
+        return (np.abs(_bf16(ds @ k.astype(f) * scale) - want) / err)[128:].max()
+
+    assert worst((p * dp).sum(-1, keepdims=True)) < 1
+    assert worst((o.astype(f) * do.astype(f)).sum(-1, keepdims=True)) > 2
