@@ -15,6 +15,8 @@ import torch
 from gated_delta_rule_04_amd import mla
 from oracle import mla as orc
 
+from ._paged_cases import marked, run_length
+
 pytestmark = pytest.mark.gpu
 
 BF16 = torch.bfloat16
@@ -237,6 +239,98 @@ def test_paged_chunk_spans_many_row_blocks():
 def test_paged_long_cache_is_split():
     _check_paged("long", *_paged(9, [20000], 64, 8, 128, 64), 128)
     _check_paged("long ragged", *_paged(10, [9000, 3, 0, 2500], 64, 4, 512, 64), 512)
+
+
+def _check_all_rows(tag, q, cache, table, lens, cu, R, scale, run=None):
+    """Every row of a large call against float64 on the GPU, within the bounds of oracle.mla.attend."""
+    if run is not None:  # the shapes give each workgroup at least this many tiles in a row
+        assert run_length(lens, None if cu is None else np.diff(cu), q.shape[1], R, cache.shape[1], table.shape[1])[1] >= run
+    Tq, H, D = q.shape
+    dq, dc, dt, dl = _cuda(q, cache, _i32(table), _i32(lens))
+    o, lse = mla.paged_attn(dq, dc, dt, dl, R, scale, cu_seqlens=None if cu is None else _i32(cu).cuda())
+    torch.cuda.synchronize()
+    print("DONE", tag, flush=True)
+    starts = np.arange(len(lens) + 1) if cu is None else cu
+    worst = [0.0, 0.0]
+    for n, L in enumerate(lens):
+        b, e, L = int(starts[n]), int(starts[n + 1]), int(L)
+        if e == b:
+            continue
+        j = torch.arange(L, device="cuda")
+        page = dt[n].long()[j // cache.shape[1]]
+        there = (page >= 0) & (page < cache.shape[0])
+        k = dc[page.clamp(0, cache.shape[0] - 1), j % cache.shape[1]].double() * there[:, None]
+        qq = dq[b:e].double().reshape(-1, D)
+        tok = torch.arange(e - b, device="cuda").repeat_interleave(H)
+        sees = there & (j <= (L - (e - b) + tok)[:, None])
+        s = (qq @ k.T * scale).masked_fill(~sees, -float("inf"))
+        es = ((D + 16) * orc.U * scale * (qq.abs() @ k.abs().T)).masked_fill(~sees, 0.0)
+        lse64 = torch.logsumexp(s, -1) if L else torch.full((len(qq),), -float("inf"), device="cuda").double()
+        empty = torch.isinf(lse64)
+        p = torch.exp(s - lse64.masked_fill(empty, 0.0)[:, None])
+        want, mag = p @ k[:, :R], p @ k[:, :R].abs()
+        w = es.amax(-1, keepdim=True) if L else es.sum(-1, keepdim=True)
+        err = (orc.E + 2 * w + (64 + L) * orc.U) * mag + orc.E * want.abs()
+        err_l = w[:, 0] + (64 + L) * orc.U + 4 * orc.U * lse64.masked_fill(empty, 0.0).abs()
+        got, got_l = o[b:e].double().reshape(-1, R), lse[b:e].double().reshape(-1)
+        assert bool((got_l[empty] == -float("inf")).all()) and bool((got[empty] == 0).all()), (tag, n)
+        off, off_l = (got - want).abs(), (got_l - lse64)[~empty].abs()
+        assert bool((off <= err + 1e-30).all()) and bool((off_l <= err_l[~empty]).all()), (tag, n, float((off / (err + 1e-30)).max()))
+        worst = [max(worst[0], float((off / (err + 1e-30)).max())), max([worst[1], *(off_l / err_l[~empty]).tolist()])]
+    print("BOUND %-28s of its bound at most %.2f, lse %.2f" % (tag, *worst), flush=True)
+
+
+def _many(R, seed, hi=6000):
+    """Lengths whose tiles are more than 32 times the workgroups', short and empty sequences among them."""
+    lens = np.random.default_rng(seed).integers(1, hi + 1, 420 if R == 128 else 220)
+    lens[3::17] = lens[3::17] % 200
+    lens[5], lens[40] = 0, hi
+    return lens
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+@pytest.mark.parametrize("H,page", [(5, 16), (40, 64), (96, 100)])
+def test_paged_long_runs_of_tiles(R, Dr, H, page):
+    """Runs of more than 32 tiles a workgroup, over the ends of sequences, in blocks of 32, 64 and 128 rows."""
+    print("CASE runs", R, Dr, H, page, flush=True)
+    lens = _many(R, H)
+    _check_all_rows("runs H%d R%d" % (H, R), *marked(H + R, lens, page, H, R, Dr, pool=9), R, 0.1, run=33)
+
+
+@pytest.mark.parametrize("H", [5, 40, 96])
+def test_paged_long_runs_with_missing_pages(H):
+    print("CASE runs, missing", H, flush=True)
+    q, cache, table, lens, cu = marked(71 + H, _many(512, H + 1), 24, H, 512, 64, pool=9)
+    r = np.random.default_rng(H)
+    gone = r.random(table.shape) < 0.03
+    table[gone] = r.choice([-1, cache.shape[0], 1 << 30], int(gone.sum()))
+    _check_all_rows("missing H%d" % H, q, cache, table, lens, cu, 512, 0.1, run=33)
+
+
+@pytest.mark.parametrize("R,Dr,H", [(512, 64, 5), (512, 0, 40), (512, 64, 96), (256, 64, 12), (128, 0, 8)])
+def test_paged_long_runs_of_rising_scores(R, Dr, H):
+    print("CASE runs, rising", R, Dr, H, flush=True)
+    _check_all_rows("rising H%d R%d" % (H, R), *marked(81 + H, _many(R, H + 2), 64, H, R, Dr, pool=9, rise=(0.05, 4.0)), R,
+                    0.3, run=33)
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_long_runs_of_chunks(R, Dr):
+    """Several row blocks a sequence, each a run of tiles or more."""
+    print("CASE runs, chunks", R, Dr, flush=True)
+    r = np.random.default_rng(R + Dr)
+    N = 48 if R == 128 else 24
+    q_lens = r.integers(0, 90, N)
+    lens = np.maximum(r.integers(1500, 6000, N), q_lens)
+    lens[2], lens[7] = q_lens[2], q_lens[7] // 2  # a first chunk, and one with rows that see nothing
+    _check_all_rows("chunks R%d" % R, *marked(91 + R, lens, 24, 16, R, Dr, q_lens=q_lens, pool=9), R, 0.1, run=17)
+
+
+@pytest.mark.parametrize("R,Dr,H,lens", [(128, 0, 8, [20000]), (512, 64, 12, [131072]), (256, 0, 64, [70000, 900]),
+                                         (512, 64, 96, [30000, 0, 41000])])
+def test_paged_every_part_of_a_long_cache(R, Dr, H, lens):
+    print("CASE parts", R, H, lens, flush=True)
+    _check_all_rows("parts R%d" % R, *marked(101 + H, lens, 64, H, R, Dr, pool=3), R, 0.1)
 
 
 def test_paged_scores_that_rise_and_large_ones():

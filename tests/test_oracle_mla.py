@@ -8,6 +8,8 @@ import torch
 
 from oracle import mla as orc
 
+from ._paged_cases import marked
+
 
 def _rng(seed):
     return np.random.default_rng(seed)
@@ -144,3 +146,23 @@ def test_bounds_tell_a_delta_of_the_rounded_output(mul):
 
     assert worst((p * dp).sum(-1, keepdims=True)) < 1
     assert worst((o.astype(f) * do.astype(f)).sum(-1, keepdims=True)) > 2
+
+
+def test_bounds_tell_every_lost_part_of_a_long_cache():
+    """A cache of 20,000 rows attended in parts of 64 rows and joined: any part's sums lost, or taken twice, are
+    outside the bounds (planted mistakes); the join of all is inside."""
+    R, page, L, H = 128, 64, 20000, 2
+    q, cache, table, lens, _ = marked(9, [L], page, H, R, 0, pool=3)
+    want, _, err, _ = orc.paged_attention(q, cache, table, lens, R, 0.1)
+    k = orc.paged_rows(cache, table[0], L)[0]
+    for h in range(H):
+        s = k @ q[0, h].double().numpy() * 0.1
+        w = np.exp(s - s.max())
+        p = _bf16(w)  # weights are rounded as operands
+        parts = np.stack([p[j:j + 64] @ k[j:j + 64] for j in range(0, L, 64)]) / w.sum()
+        off = np.abs(_bf16(parts.sum(0)) - want[0, h])
+        assert (off <= err[0, h]).all()
+        assert (off[R // 2:] <= 0.02 * want[0, h, R // 2:]).all()
+        for part in parts:
+            for wrong in (parts.sum(0) - part, parts.sum(0) + part):
+                assert (np.abs(wrong - want[0, h]) > 2 * err[0, h]).any()
