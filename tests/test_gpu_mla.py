@@ -127,6 +127,15 @@ def test_expanded_odd_heads_and_batch():
     _check_expanded("H13 B5", *_expanded(22, 5, 70, 13, 64, 0))
 
 
+@pytest.mark.parametrize("Dn,Dr", HEADS)
+def test_expanded_heads_by_eights_and_many_tiles(Dn, Dr):
+    """Heads (times batch rows) that are a multiple of 8, several tiles each: a launch order of its own."""
+    print("CASE eights", Dn, Dr, flush=True)
+    _check_expanded("H8", *_expanded(25, 1, 300, 8, Dn, Dr))
+    _check_expanded("B3 H8", *_expanded(26, 3, 300, 8, Dn, Dr))
+    _check_expanded("H16 docs", *_expanded(27, 1, 420, 16, Dn, Dr), cu=[0, 140, 140, 141, 410])
+
+
 def test_expanded_most_heads():
     _check_expanded("H 1024", *_expanded(24, 1, 40, 1024, 64, 0))
 
