@@ -140,6 +140,47 @@ def test_expanded_most_heads():
     _check_expanded("H 1024", *_expanded(24, 1, 40, 1024, 64, 0))
 
 
+def test_expanded_offsets_past_32_bits():
+    """Packed documents whose q, kv, o and gradients pass 2^31 elements: the last ones are as when they are alone."""
+    H, Dn, Dr, doc, last = 96, 128, 64, 230, 610
+    n = (1 << 31) // (H * Dn * doc) + 1  # documents ahead, so that o passes 2^31 elements too
+    cu = np.concatenate([np.arange(n + 1) * doc, n * doc + np.array([77, 77, last])])
+    T = int(cu[-1])
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=BF16)  # noqa: E731
+    q, kv, pe, do = rnd(1, T, H, Dn + Dr), rnd(1, T, H, 2 * Dn), rnd(1, T, Dr), rnd(1, T, H, Dn)
+    assert do.numel() > 1 << 31
+
+    def run(args, cu):
+        cu = _i32(cu).cuda()
+        o, lse = mla.attn_fwd(*args[:3], cu_seqlens=cu)
+        return [o, lse, *mla.attn_bwd(*args[:3], o, lse, args[3], cu_seqlens=cu).values()]
+
+    end = [t[:, n * doc:].clone() for t in (q, kv, pe, do)]
+    for a, b in zip(run((q, kv, pe, do), cu), run(end, cu[n:] - n * doc)):
+        assert torch.equal(a[:, n * doc:], b) and bool(torch.isfinite(b.float()).all())
+
+
+def test_calls_without_a_log_sum_exp():
+    """lse is optional in the library: the outputs are the same bits without it."""
+    ptr = lambda t: t.data_ptr()  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    q, kv, pe, _ = _cuda(*_expanded(71, 1, 200, 3, 128, 64))
+    o, _ = mla.attn_fwd(q, kv, pe)
+    got = torch.empty_like(o)
+    assert mla.lib().kda_mla_attn_fwd(ptr(q), ptr(kv), ptr(pe), ptr(got), None, None, 1, 1, 200, 3, 128, 64, 128,
+                                      192 ** -0.5, mla.KDA_BF16, stream) == 0
+    assert torch.equal(o, got)
+    q, cache, table, lens, _ = _paged(72, [300, 20000], 64, 5, 128, 64)
+    q, cache, table, lens = _cuda(q, cache, _i32(table), _i32(lens))
+    o, _ = mla.paged_attn(q, cache, table, lens, 128, 0.1)
+    need = mla.paged_workspace_bytes(2, 2, 5, 128, 64, 64, table.shape[1])
+    got, ws = torch.empty_like(o), torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert mla.lib().kda_mla_paged_attn(ptr(q), ptr(cache), ptr(table), ptr(lens), None, ptr(got), None, 2, 2, 5, 128, 64,
+                                        cache.shape[0], 64, table.shape[1], 0.1, mla.KDA_BF16, ptr(ws), need, stream) == 0
+    assert torch.equal(o, got)
+
+
 def test_expanded_other_documents_do_not_matter():
     cu, T = [0, 90, 170, 300], 300
     q, kv, pe, do = _expanded(31, 1, T, 2, 128, 64)
@@ -382,6 +423,30 @@ def test_paged_many_sequences():
     lens = r.integers(0, 90, 700).tolist()
     _check_paged("700 single", *_paged(23, lens, 16, 2, 128, 64), 128)
     _check_paged("700 chunks", *_paged(24, lens, 16, 2, 128, 0, q_lens=r.integers(0, 4, 700).tolist(), pad=3), 128)
+
+
+@pytest.mark.parametrize("R,Dr,H", [(128, 64, 1), (512, 0, 80)])
+def test_paged_most_sequences(R, Dr, H):
+    """65,536 sequences of one cache row or none (with 80 heads of 512 channels, offsets of q and o past 2^31): a row
+    that sees one row gives its latent, exactly."""
+    print("CASE most sequences", R, H, flush=True)
+    N, pages, page = 1 << 16, 300, 4
+    g = torch.Generator(device="cuda").manual_seed(R)
+    cache = torch.randn((pages, page, R + Dr), generator=g, device="cuda").to(BF16)
+    table = torch.randint(0, pages, (N, 2), generator=g, device="cuda", dtype=torch.int32)
+    lens = (torch.rand(N, generator=g, device="cuda") < 0.8).to(torch.int32)
+    q = torch.randn((N, H, R + Dr), generator=g, device="cuda", dtype=BF16)
+    o, lse = mla.paged_attn(q, cache, table, lens, R, 0.05)
+    for b in range(0, N, 4096):
+        x = slice(b, b + 4096)
+        one = lens[x, None, None] == 1
+        row = cache[table[x, 0].long(), 0]
+        assert torch.equal(o[x], torch.where(one, row[:, None, :R], torch.zeros((), dtype=BF16, device="cuda")).expand(-1, H, -1))
+        s = (q[x].float() * row[:, None].float()).sum(-1) * 0.05
+        mag = (q[x].float() * row[:, None].float()).abs().sum(-1) * 0.05
+        off = (lse[x] - s).abs() - (2 * (R + Dr + 16) * orc.U * mag + 64 * orc.U)  # two float32 sums
+        assert bool((torch.where(one[..., 0], off, -torch.ones_like(off)) <= 0).all())
+        assert bool(torch.isneginf(lse[x][lens[x] == 0]).all())
 
 
 def test_paged_most_heads():
