@@ -425,7 +425,10 @@ kda_status kda_short_conv_step(const void* x, const void* weight, void* conv_sta
  *
  * Shared by the five calls: dt is KDA_BF16 (KDA_F32 and KDA_F16 return
  * KDA_ERR_UNSUPPORTED); scores, softmax statistics, sums and log-sum-exps
- * are float32, results are rounded once at the end; 1 <= H <= 1024; every
+ * are float32.  The softmax weights, and the backward's dS, are rounded to
+ * bf16 as operands of the products that sum them (a row's sum of weights and
+ * its <dout, o> are taken from the unrounded ones); results are rounded at the
+ * end.  1 <= H <= 1024; every
  * bf16 and float tensor 16-byte aligned, a workspace 256-byte aligned
  * (KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE).  scale must be finite and
  * positive (KDA_ERR_SHAPE).  A non-finite value may reach every row of its
