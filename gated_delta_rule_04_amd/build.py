@@ -46,7 +46,8 @@ SOURCE_FLAGS = {
     # Matrix instructions selected with vector-register results leave the
     # allocator free to keep long-lived sums in either half of the register
     # file: without it the paged attention's 256 registers of sums at 512
-    # channels spill (600 registers), and dk, dv take 466 registers, not 321.
+    # channels spill (513 registers; 14 with it), and dk, dv at 128 + 64
+    # channels take 380 registers, not 339.
     "mla_paged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "mla_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }

@@ -9,10 +9,11 @@
 // pass over both directions would add dq in an order that changes from run to
 // run, or keep it in a workspace of float32 tiles).  p and ds are rounded to
 // bf16 as operands; sums are float32.
-// B1 T16384 H12 128/64: delta 0.92 ms (three workgroups a CU; tiles of 64 keys at
-// two a CU 1.07), dq 1.53 ms, dk and dv 2.2 to 2.3 ms (the sums and operands of
-// 32 keys are 339 registers, so one wavefront a SIMD; 2.6 ms before the next
-// tile's scores were formed beside the weights), dk_pe's sum 9 us.
+// B1 T16384 H12 128/64: delta 0.89 to 0.93 ms by GPU (three workgroups a CU,
+// matrix units 70% busy; tiles of 64 keys at two a CU 1.07), dq 1.51 to 1.57 ms
+// (57%), dk and dv 2.2 to 2.6 ms (39%: the sums and operands of 32 keys are 339
+// registers, so one wavefront a SIMD; a fifth more before the next tile's scores
+// were formed beside the weights), dk_pe's sum 9 us.
 
 #include <math.h>
 
@@ -177,8 +178,9 @@ __global__ __launch_bounds__(256, 2) void dq_kernel(AttnArgs a, TileMap map) {
 // dk and dv: S = Q K^T with the wavefront's 32 keys as B operands in registers,
 // so that P and dS come as B operands over the queries; dV^T += dO^T P and
 // dK^T += Q^T dS.  The rotary part of dk is this head's share of dk_pe.
-// Up to 128 channels two wavefronts a SIMD (B4 T4096 H16 128/0: backward 1.20 ->
-// 1.15 ms); at 128 / 64 their 256 registers spill (3.8 -> 6.6 ms at T16384 H12).
+// Up to 128 channels two wavefronts a SIMD (B4 T4096 H16 128/0: backward 1.15 ms
+// where one takes 1.20, though 12 of their 256 registers spill); at 128 / 64 too
+// many do (3.8 -> 6.6 ms at T16384 H12; both before delta had its own kernel).
 template <int DN, int DR>
 __global__ __launch_bounds__(256, DN + DR <= 128 ? 2 : 1) void dkv_kernel(AttnArgs a, TileMap map) {
   constexpr int DQ = DN + DR;

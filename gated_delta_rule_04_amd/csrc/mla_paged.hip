@@ -19,9 +19,15 @@
 // so that both the row reads and the transposing reads spread over the banks.
 
 // N256 H8 R256 rows to 2,048: 44 us (4.0 TB/s, a copy moving 5.1); N64 H96
-// R512+64 to 8,192: 149 us; 4 chunks of up to 512 tokens at H96: 2.7 ms (840
-// TFLOP/s).  Bound by memory for few heads; with 128 rows a block by the
-// products and the softmax of one wavefront a SIMD in turn.
+// R512+64 to 8,192: 151 us; 4 chunks of up to 512 tokens at H96: 2.7 to 2.8 ms
+// (matrix units 23% and 35% busy).  Bound by memory for few heads; at R = 512
+// nearly every product waits for its own operand from LDS (62 of 68 in the code
+// of 128-row blocks), and one wavefront a SIMD has nothing else to do then.
+// Units count a sequence's whole cache, while a block of a causal chunk stops at
+// the last row it sees: the longest run of a first chunk (no cache before it)
+// has up to twice the mean's work (4 x 512 tokens, H96: 393 us).  Each workgroup
+// goes through all the sequences' lengths to find its run: 65,536 sequences of
+// 16 rows, H1 R128, take 0.9 ms, 4,096 of them 61 us.
 
 #include <limits.h>
 #include <math.h>
@@ -42,10 +48,13 @@ struct PagedPlan {
 };
 
 // Block height by the rows a sequence has, the smallest that holds them or 128:
-// a low block leaves fewer rows of its products empty (N64 R512+64 to 8,192:
-// H12 in blocks of 32 144 us, H64 in blocks of 64 155 us), a high one reads each
-// tile once for more rows (H96 in one block of 128 225 us, in two of 64 243 us;
-// chunks of 512 tokens 4.1 and 4.6 ms).  Workgroups: as many as run at once (by
+// a low block leaves fewer rows of its products empty, a high one reads each
+// tile once for more rows.  In blocks of 32 / 64 / 128 rows, N64, all of 8,192
+// cache rows, R 512+64: H12 158 / 171 / 203 us, H64 234 / 165 / 200, H96 367 /
+// 271 / 216; chunks of 4 x 512 tokens, H96: 8.9 / 5.2 / 4.3 ms.  (R 256, 4,096
+// rows: H12 42 / 46 / 65 us, H64 60 / 49 / 69, H96 86 / 73 / 73.  At R 128, where
+// 64 rows are no slower for H96, 52 against 57 us, the chunks still gain: 1.33
+// and 1.11 ms.)  Workgroups: as many as run at once (by
 // their LDS one a CU at R = 512 and 256, two at 128), or the units there can be.
 PagedPlan paged_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   PagedPlan p;
