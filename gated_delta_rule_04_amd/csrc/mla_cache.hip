@@ -1,5 +1,6 @@
-// Append of new tokens to the paged latent cache: RMS norm of the latent,
-// rotation of the rotary key, rotation of the queries' rotary parts.
+// Append of new tokens to the paged latent cache, in bf16 or in 4 bits: RMS norm
+// of the latent, rotation of the rotary key, rotation of the queries' rotary
+// parts; and the gather that reads 4-bit rows back.
 //
 // Memory bound: each row is read once and written once, 2 (R + Dr) bytes a
 // token each way, and 2 Dr bytes a query head each way: 185 MB at 32,768
@@ -9,7 +10,7 @@
 // in float32 over lane shuffles), the others rotations (8 pairs a thread: two
 // 16-byte loads and stores, the table row as 32-byte loads).
 
-#include "mla_launch.h"
+#include "mla_fp4.h"
 
 namespace mla {
 namespace {
@@ -24,11 +25,91 @@ __device__ __forceinline__ bool kept(const AppendArgs& a, int t, int& slot) {
   return (unsigned)slot < (unsigned)a.num_slots;
 }
 
+// A latent row in 4 bits.  R / 32 lanes a row, a block of 32 channels a lane, so
+// that a lane has all that its scale needs.  Everything up to the code is float64,
+// in which it costs no more than float32 here (both units take a lane a cycle, and
+// the row's bytes bound the pass): a relative error of 2^-50 in place of 2^-22 in
+// a value beside a border of its code decides a whole step of the code, which would
+// otherwise happen to a value in about 10^6.  The float64 value divided by 2^E goes
+// to the conversion instruction (float32 to 4 bits, ties to even) as 21 bits of
+// its mantissa with what lies below or-ed into the last of them, which rounds as
+// the whole would: the borders have 3 bits.
 template <int R, int DR>
+__device__ __forceinline__ void append_latent_fp4(const AppendArgs& a, int block) {
+  constexpr int kLanes = R / 32, kRows = kThreads / kLanes;
+  const long long t = (long long)block * kRows + threadIdx.x / kLanes;
+  const int c = threadIdx.x % kLanes;
+  int slot = 0;
+  const bool on = t < a.T && kept(a, (int)t, slot);
+  double y[32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bf16x8 x = {};
+    if (on) x = *(const bf16x8*)(a.c + t * (R + DR) + c * 32 + 8 * i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[8 * i + j] = (double)(float)x[j];
+  }
+  if (a.weight) {
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) ss += y[i] * y[i];
+#pragma unroll
+    for (int m = 1; m < kLanes; m <<= 1) ss += __shfl_xor(ss, m);
+    const double r = 1.0 / sqrt(ss * (1.0 / R) + (double)a.eps);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const f32x4 w = *(const f32x4*)(a.weight + c * 32 + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[i + j] = y[i + j] * r * (double)w[j];
+    }
+  }
+  if (!on) return;
+  // the upper word of |y|, the last bit set for anything below it
+  auto upper = [](double x) {
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, x);
+    return (unsigned)(b >> 32) | ((unsigned)b != 0);
+  };
+  unsigned most = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) most = max(most, upper(y[i]) & 0x7fffffffu);
+  // max |y| = (1 + f) 2^k <= 7 2^E
+  int e = (int)(most >> 20) - 1023 - 2 + ((most & 0xfffffu) > 0xc0000u);
+  const bool finite = most < 0x7ff00000u;
+  e = min(max(e, -125), 125);
+  const double inv = __builtin_bit_cast(double, (unsigned long long)(1023 - e) << 52);
+  unsigned code[4] = {};
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const unsigned long long b = (unsigned long long)upper(y[i + j]) << 32;
+      v[j] = (float)(__builtin_bit_cast(double, b) * inv);
+    }
+    switch (i / 2 % 4) {
+      case 0: code[i / 8] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code[i / 8], v[0], v[1], 1.f, 0); break;
+      case 1: code[i / 8] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code[i / 8], v[0], v[1], 1.f, 1); break;
+      case 2: code[i / 8] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code[i / 8], v[0], v[1], 1.f, 2); break;
+      default: code[i / 8] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code[i / 8], v[0], v[1], 1.f, 3);
+    }
+  }
+  if (!finite) code[0] = code[1] = code[2] = code[3] = 0;
+  constexpr int kRow = fp4_row_bytes(R, DR), kScales = R / 2 + 2 * DR;
+  unsigned char* row = (unsigned char*)a.cache + (long long)slot * kRow;
+  *(u32x4*)(row + c * 16) = u32x4{code[0], code[1], code[2], code[3]};
+  row[kScales + c] = (unsigned char)(finite ? e + 127 : 255);
+  for (int i = kScales + kLanes + c; i < kRow; i += kLanes) row[i] = 0;
+}
+
+template <int R, int DR, bool FP4>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int latent_blocks) {
   constexpr int kLanes = R / 8;              // lanes of a latent row
   constexpr int kRows = kThreads / kLanes;   // latent rows of a block
   if ((int)blockIdx.x < latent_blocks) {
+    if constexpr (FP4) {
+      append_latent_fp4<R, DR>(a, blockIdx.x);
+      return;
+    }
     const long long t = (long long)blockIdx.x * kRows + threadIdx.x / kLanes;
     const int c = threadIdx.x % kLanes;
     int slot = 0;
@@ -46,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int late
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = (bf16)((float)x[i] * r * (i < 4 ? w0[i & 3] : w1[i & 3]));
     }
-    if (on) *(bf16x8*)(a.cache + (long long)slot * (R + DR) + c * 8) = x;
+    if (on) *(bf16x8*)((bf16*)a.cache + (long long)slot * (R + DR) + c * 8) = x;
     return;
   }
   if constexpr (DR > 0) {
@@ -65,7 +146,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int late
       int slot;
       if (!kept(a, (int)t, slot)) return;
       src = a.c + t * (R + DR) + R;
-      dst = a.cache + (long long)slot * (R + DR) + R;
+      dst = FP4 ? (bf16*)((char*)a.cache + (long long)slot * fp4_row_bytes(R, DR) + R / 2)
+                : (bf16*)a.cache + (long long)slot * (R + DR) + R;
     } else {
       src = a.q_pe + (t * a.H + h - 1) * DR;
       dst = a.q + (t * a.H + h - 1) * (R + DR) + R;
@@ -108,26 +190,87 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int late
   }
 }
 
+// Rows of a 4-bit cache as bf16: R / 8 lanes a row, 8 channels a lane (4 bytes in,
+// 16 out), the rotary key by the first 8 of them.
 template <int R, int DR>
-hipError_t launch(const AppendArgs& a, hipStream_t stream) {
+__global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
+  constexpr int kLanes = R / 8, kRows = kThreads / kLanes, kRow = fp4_row_bytes(R, DR);
+  const long long t = (long long)blockIdx.x * kRows + threadIdx.x / kLanes;
+  const int c = threadIdx.x % kLanes;
+  if (t >= min(max(a.cu[a.N], 0), a.T)) return;
+  int lo = 0, hi = a.N;
+  while (hi - lo > 1) {  // the last sequence that starts at or before the row
+    const int mid = lo + (hi - lo) / 2;
+    if (min(max(a.cu[mid], 0), a.T) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const long long j = t - min(max(a.cu[lo], 0), a.T) + (a.starts ? a.starts[lo] : 0);
+  const unsigned char* row = nullptr;
+  if (j >= 0 && j < (long long)a.max_pages * a.page_size) {
+    const unsigned p = (unsigned)j / (unsigned)a.page_size;
+    const int page = a.table[(long long)lo * a.max_pages + p];
+    if ((unsigned)page < (unsigned)a.num_pages)
+      row = a.cache + ((long long)page * a.page_size + ((unsigned)j - p * a.page_size)) * kRow;
+  }
+  u32x4 v = {}, pe = {};
+  if (row) {
+    const unsigned codes = *(const unsigned*)(row + 4 * c);
+    v = fp4_values(codes, __builtin_bit_cast(float, (unsigned)row[R / 2 + 2 * DR + c / 4] << 23));
+    if (DR && c < DR / 8) pe = *(const u32x4*)(row + R / 2 + 16 * c);
+  }
+  bf16* out = a.rows + t * (R + DR);
+  *(u32x4*)(out + 8 * c) = v;
+  if (DR && c < DR / 8) *(u32x4*)(out + R + 8 * c) = pe;
+}
+
+template <int R, int DR>
+hipError_t launch_gather(const GatherArgs& a, hipStream_t stream) {
   constexpr int kRows = kThreads / (R / 8);
+  gather_kernel<R, DR><<<dim3((unsigned)((a.T + kRows - 1) / kRows)), dim3(kThreads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int R, int DR, bool FP4>
+hipError_t launch(const AppendArgs& a, hipStream_t stream) {
+  constexpr int kRows = kThreads / (R / (FP4 ? 32 : 8));
   const int latent = (a.T + kRows - 1) / kRows;
   const long long units = DR ? (long long)a.T * (a.H + 1) * (DR / 16) : 0;
   const long long blocks = latent + (units + kThreads - 1) / kThreads;
-  append_kernel<R, DR><<<dim3((unsigned)blocks), dim3(kThreads), 0, stream>>>(a, latent);
+  append_kernel<R, DR, FP4><<<dim3((unsigned)blocks), dim3(kThreads), 0, stream>>>(a, latent);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_append(int R, int Dr, const AppendArgs& a, hipStream_t stream) {
+template <bool FP4>
+static hipError_t launch_append(int R, int Dr, const AppendArgs& a, hipStream_t stream) {
   switch (R + Dr) {
-    case 128: return launch<128, 0>(a, stream);
-    case 192: return launch<128, 64>(a, stream);
-    case 256: return launch<256, 0>(a, stream);
-    case 320: return launch<256, 64>(a, stream);
-    case 512: return launch<512, 0>(a, stream);
-    case 576: return launch<512, 64>(a, stream);
+    case 128: return launch<128, 0, FP4>(a, stream);
+    case 192: return launch<128, 64, FP4>(a, stream);
+    case 256: return launch<256, 0, FP4>(a, stream);
+    case 320: return launch<256, 64, FP4>(a, stream);
+    case 512: return launch<512, 0, FP4>(a, stream);
+    case 576: return launch<512, 64, FP4>(a, stream);
+  }
+  return hipErrorInvalidValue;
+}
+hipError_t launch_append(int R, int Dr, const AppendArgs& a, hipStream_t stream) {
+  return launch_append<false>(R, Dr, a, stream);
+}
+hipError_t launch_append_fp4(int R, int Dr, const AppendArgs& a, hipStream_t stream) {
+  return launch_append<true>(R, Dr, a, stream);
+}
+
+hipError_t launch_gather(int R, int Dr, const GatherArgs& a, hipStream_t stream) {
+  switch (R + Dr) {
+    case 128: return launch_gather<128, 0>(a, stream);
+    case 192: return launch_gather<128, 64>(a, stream);
+    case 256: return launch_gather<256, 0>(a, stream);
+    case 320: return launch_gather<256, 64>(a, stream);
+    case 512: return launch_gather<512, 0>(a, stream);
+    case 576: return launch_gather<512, 64>(a, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -20,17 +20,53 @@ struct AppendArgs {
   int interleaved;
   const int* positions;
   const int* slots;
-  bf16* cache;          // [num_slots][R + Dr]
+  void* cache;          // [num_slots] rows: bf16 [R + Dr], or fp4_row_bytes(R, Dr) bytes
   int num_slots;
   const bf16* q_pe;     // [T][H][Dr] or NULL
   bf16* q;              // [T][H][R + Dr]
   int T, H;
 };
 hipError_t launch_append(int R, int Dr, const AppendArgs& a, hipStream_t stream);
+hipError_t launch_append_fp4(int R, int Dr, const AppendArgs& a, hipStream_t stream);
+
+// A row of the 4-bit cache: codes, rotary key, scales, zeros to a multiple of 16.
+__host__ __device__ constexpr int fp4_row_bytes(int R, int Dr) { return (R / 2 + 2 * Dr + R / 32 + 15) / 16 * 16; }
+
+struct GatherArgs {
+  const unsigned char* cache;  // [num_pages * page_size][fp4_row_bytes]
+  const int* table;            // [N][max_pages]
+  const int* cu;               // [N + 1]
+  const int* starts;           // [N] or NULL
+  bf16* rows;                  // [T][R + Dr]
+  int N, T, num_pages, page_size, max_pages;
+};
+hipError_t launch_gather(int R, int Dr, const GatherArgs& a, hipStream_t stream);
+
+struct PlanArgs {
+  const int *new_lens, *seq_lens;  // [N]
+  int* table;                      // [N][max_pages]
+  const int *free_pages, *free_count;
+  int *cu, *positions, *slots, *kv_lens, *lens_out, *free_out;
+  int* top;                        // workspace [N]: where a sequence's first new page lies in the list
+  int num_free, N, T, page_size, max_pages, capacity;
+};
+hipError_t launch_plan(const PlanArgs& p, hipStream_t stream);
+
+struct ReleaseArgs {
+  const unsigned char* finished;  // [N]
+  const int *seq_lens, *table;
+  int* free_pages;
+  const int* free_count;
+  int *lens_out, *free_out;
+  int* first;                     // workspace [N + 2]: ends of the sequences' pages in the list, and the list's old end
+  int num_free, N, page_size, max_pages, capacity;
+};
+hipError_t launch_release(const ReleaseArgs& p, hipStream_t stream);
 
 struct PagedArgs {
   const bf16* q;      // [Tq][H][R + Dr]
   const bf16* cache;  // [num_pages * page_size][R + Dr]
+  const unsigned char* cache4;  // or [num_pages * page_size][fp4_row_bytes]
   const int* table;   // [N][max_pages]
   const int* lens;    // [N]
   const int* cu;      // [N + 1] or NULL: one token a sequence
@@ -42,6 +78,8 @@ struct PagedArgs {
 };
 size_t paged_workspace(int N, int Tq, int H, int R, int Dr, long long max_len);
 hipError_t launch_paged(int R, int Dr, const PagedArgs& a, hipStream_t stream);
+size_t paged_fp4_workspace(int N, int Tq, int H, int R, int Dr, long long max_len);
+hipError_t launch_paged_fp4(int R, int Dr, const PagedArgs& a, hipStream_t stream);
 
 // Expanded form.  Tokens are counted through the batch (b * T + t); documents
 // come from cu, or are the rows of the batch when cu is NULL.

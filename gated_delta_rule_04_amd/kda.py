@@ -34,6 +34,9 @@ EXPORTED = ["kda_chunk_fwd_workspace_bytes", "kda_chunk_fwd", "kda_chunk_fwd_noa
             "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_bytes", "kda_short_conv_bwd", "kda_short_conv_step",
             "kda_mla_cache_append", "kda_mla_paged_workspace_bytes", "kda_mla_paged_attn", "kda_mla_attn_fwd",
             "kda_mla_attn_bwd_workspace_bytes", "kda_mla_attn_bwd",
+            "kda_mla_cache_plan_workspace_bytes", "kda_mla_cache_plan", "kda_mla_cache_release_workspace_bytes",
+            "kda_mla_cache_release", "kda_mla_fp4_row_bytes", "kda_mla_cache_append_fp4", "kda_mla_cache_gather_fp4",
+            "kda_mla_paged_fp4_workspace_bytes", "kda_mla_paged_attn_fp4",
             "kda_status_str", "kda_abi_version"]
 
 _lib = None
@@ -108,6 +111,24 @@ def lib():
     L.kda_mla_attn_bwd_workspace_bytes.argtypes = [i] * 8
     L.kda_mla_attn_bwd.restype = i
     L.kda_mla_attn_bwd.argtypes = [vp] * 10 + [i] * 7 + [f, i, vp, sz, vp]
+    L.kda_mla_cache_plan_workspace_bytes.restype = sz
+    L.kda_mla_cache_plan_workspace_bytes.argtypes = [i]
+    L.kda_mla_cache_plan.restype = i
+    L.kda_mla_cache_plan.argtypes = [vp] * 5 + [i] + [vp] * 6 + [i] * 4 + [vp, sz, vp]
+    L.kda_mla_cache_release_workspace_bytes.restype = sz
+    L.kda_mla_cache_release_workspace_bytes.argtypes = [i]
+    L.kda_mla_cache_release.restype = i
+    L.kda_mla_cache_release.argtypes = [vp] * 5 + [i, vp, vp, i, i, i, vp, sz, vp]
+    L.kda_mla_fp4_row_bytes.restype = sz
+    L.kda_mla_fp4_row_bytes.argtypes = [i, i]
+    L.kda_mla_cache_append_fp4.restype = i
+    L.kda_mla_cache_append_fp4.argtypes = L.kda_mla_cache_append.argtypes
+    L.kda_mla_cache_gather_fp4.restype = i
+    L.kda_mla_cache_gather_fp4.argtypes = [vp] * 5 + [i] * 8 + [vp]
+    L.kda_mla_paged_fp4_workspace_bytes.restype = sz
+    L.kda_mla_paged_fp4_workspace_bytes.argtypes = [i] * 8
+    L.kda_mla_paged_attn_fp4.restype = i
+    L.kda_mla_paged_attn_fp4.argtypes = L.kda_mla_paged_attn.argtypes
     _lib = L
     return L
 

@@ -7,6 +7,13 @@ as in ``kda``; there is no fallback.
     o, lse = attn_fwd(q, kv, k_pe, scale=None, cu_seqlens=None)
     grads = attn_bwd(q, kv, k_pe, o, lse, do, scale=None, cu_seqlens=None)   # dq, dkv, dk_pe
 
+Pages on the device, and the cache in 4 bits:
+
+    step = cache_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, num_tokens)
+    left = cache_release(finished, seq_lens, block_table, free_pages, free_count, page_size)
+    cache_append_fp4(...), o, lse = paged_attn_fp4(...)   # as above, cache uint8 [.., fp4_row_bytes(R, Dr)]
+    rows = cache_gather_fp4(cache, block_table, cu_seqlens, num_tokens, latent_dim, starts=None)
+
 Shapes (see include/kda.h).  Absorbed (serving): a cache row is [latent of R
 channels ; rotary key of Dr channels]; c_kv [T, R + Dr]; cache [num_pages,
 page_size, R + Dr]; q [Tq, H, R + Dr]; o [Tq, H, R].  Expanded (training):
@@ -22,7 +29,9 @@ import torch
 
 from .kda import KDA_BF16, KDA_F16, KDA_F32, KdaError, _num_seqs, lib
 
-__all__ = ["cache_append", "paged_attn", "paged_workspace_bytes", "attn_fwd", "attn_bwd", "attn_bwd_workspace_bytes"]
+__all__ = ["cache_append", "paged_attn", "paged_workspace_bytes", "attn_fwd", "attn_bwd", "attn_bwd_workspace_bytes",
+           "cache_plan", "cache_release", "fp4_row_bytes", "cache_append_fp4", "cache_gather_fp4", "paged_attn_fp4",
+           "paged_fp4_workspace_bytes"]
 
 _DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.float16: KDA_F16}
 
@@ -88,20 +97,22 @@ def _workspace(workspace, need, dev):
     return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
 
 
-def cache_append(c_kv, positions, slots, cache, latent_dim, rope=None, norm_weight=None, eps=1e-6, interleaved=False,
-                 q_pe=None, q=None):
-    """Writes new tokens' rows into the paged latent cache, in place: the first
-    latent_dim channels of c_kv [T, R + Dr] RMS-normalised (norm_weight [R]
-    float32; None: as they are), the others rotated by the token's position
-    (rope [num_pos, Dr] float32: cos, then sin; None: as they are).  slots
-    int32 [T]: page * page_size + offset, outside the cache for a token that
-    is not kept.  With q_pe [T, H, Dr], q [T, H, R + Dr] gets the rotated
-    queries in its last Dr channels.  Returns cache."""
+@functools.lru_cache(maxsize=64)
+def fp4_row_bytes(latent_dim, rope_dim):
+    """Bytes of a row of the 4-bit cache."""
+    n = int(lib().kda_mla_fp4_row_bytes(latent_dim, rope_dim))
+    if n == 0:
+        raise ValueError("no 4-bit cache of %d + %d channels (128, 256 or 512 and 0 or 64)" % (latent_dim, rope_dim))
+    return n
+
+
+def _append(name, fp4, c_kv, positions, slots, cache, latent_dim, rope, norm_weight, eps, interleaved, q_pe, q):
     if c_kv.dim() != 2 or cache.dim() != 3:
         raise ValueError("c_kv must be [T, R + Dr] and cache [num_pages, page_size, R + Dr]")
     T, D = c_kv.shape
     R = int(latent_dim)
     Dr = D - R
+    row = fp4_row_bytes(R, Dr) if fp4 else D
     H = 1
     if rope is not None:
         if positions is None:
@@ -115,14 +126,35 @@ def cache_append(c_kv, positions, slots, cache, latent_dim, rope=None, norm_weig
             raise ValueError("q_pe must be [T, H, Dr]")
         H = q_pe.shape[1]
     dt, f32, i32 = c_kv.dtype, torch.float32, torch.int32
-    dev = _check(c_kv, (cache, "cache", (cache.shape[0], cache.shape[1], D), dt), (slots, "slots", (T,), i32),
-                 (positions, "positions", (T,), i32), (norm_weight, "norm_weight", (R,), f32),
+    dev = _check(c_kv, (cache, "cache", (cache.shape[0], cache.shape[1], row), torch.uint8 if fp4 else dt),
+                 (slots, "slots", (T,), i32), (positions, "positions", (T,), i32), (norm_weight, "norm_weight", (R,), f32),
                  (rope, "rope", None if rope is None else (rope.shape[0], Dr), f32), (q_pe, "q_pe", (T, H, Dr), dt),
                  (q, "q", (T, H, D), dt))
-    _call("kda_mla_cache_append", dev, _ptr(c_kv), _ptr(norm_weight), float(eps), _ptr(rope),
+    _call(name, dev, _ptr(c_kv), _ptr(norm_weight), float(eps), _ptr(rope),
           0 if rope is None else rope.shape[0], int(bool(interleaved)), _ptr(positions), _ptr(slots), _ptr(cache),
           cache.shape[0], cache.shape[1], _ptr(q_pe), _ptr(q), T, H, R, Dr, _dt(c_kv))
     return cache
+
+
+def cache_append(c_kv, positions, slots, cache, latent_dim, rope=None, norm_weight=None, eps=1e-6, interleaved=False,
+                 q_pe=None, q=None):
+    """Writes new tokens' rows into the paged latent cache, in place: the first
+    latent_dim channels of c_kv [T, R + Dr] RMS-normalised (norm_weight [R]
+    float32; None: as they are), the others rotated by the token's position
+    (rope [num_pos, Dr] float32: cos, then sin; None: as they are).  slots
+    int32 [T]: page * page_size + offset, outside the cache for a token that
+    is not kept.  With q_pe [T, H, Dr], q [T, H, R + Dr] gets the rotated
+    queries in its last Dr channels.  Returns cache."""
+    return _append("kda_mla_cache_append", False, c_kv, positions, slots, cache, latent_dim, rope, norm_weight, eps,
+                   interleaved, q_pe, q)
+
+
+def cache_append_fp4(c_kv, positions, slots, cache, latent_dim, rope=None, norm_weight=None, eps=1e-6,
+                     interleaved=False, q_pe=None, q=None):
+    """cache_append into a 4-bit cache, uint8 [num_pages, page_size, fp4_row_bytes(R, Dr)]: the latent in 4 bits with
+    a power-of-two scale for every 32 channels (include/kda.h), the rotary key in bfloat16.  Returns cache."""
+    return _append("kda_mla_cache_append_fp4", True, c_kv, positions, slots, cache, latent_dim, rope, norm_weight, eps,
+                   interleaved, q_pe, q)
 
 
 @functools.lru_cache(maxsize=256)
@@ -131,23 +163,19 @@ def paged_workspace_bytes(N, Tq, H, R, Dr, page_size, max_pages, dtype=torch.bfl
     return int(lib().kda_mla_paged_workspace_bytes(N, Tq, H, R, Dr, page_size, max_pages, _DT[dtype]))
 
 
-def paged_attn(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=None, out=None, lse=None,
-               workspace=None):
-    """Absorbed latent attention of new tokens over the paged cache.  Without
-    cu_seqlens every sequence has one new token (q [N, H, R + Dr]); with it,
-    sequence n's are rows cu[n] .. cu[n+1]-1 of q [Tq, H, R + Dr], the last of
-    its seq_lens[n] cache rows.  Returns (o [Tq, H, R], lse [Tq, H])."""
+def _paged(name, fp4, need, q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens, out, lse, workspace):
     if q.dim() != 3 or cache.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q must be [Tq, H, R + Dr], cache [num_pages, page_size, R + Dr], block_table [N, max_pages]")
+        raise ValueError("q must be [Tq, H, R + Dr], cache [num_pages, page_size, row], block_table [N, max_pages]")
     Tq, H, D = q.shape
     N, max_pages = block_table.shape
     num_pages, page_size, _ = cache.shape
     R = int(latent_dim)
+    row = fp4_row_bytes(R, D - R) if fp4 else D
     if cu_seqlens is None and N != Tq:
         raise ValueError("q must be [N, H, R + Dr], one token a sequence, without cu_seqlens")
     dt, i32 = q.dtype, torch.int32
-    dev = _check(q, (cache, "cache", (num_pages, page_size, D), dt), (block_table, "block_table", None, i32),
-                 (seq_lens, "seq_lens", (N,), i32), (cu_seqlens, "cu_seqlens", (N + 1,), i32),
+    dev = _check(q, (cache, "cache", (num_pages, page_size, row), torch.uint8 if fp4 else dt),
+                 (block_table, "block_table", None, i32), (seq_lens, "seq_lens", (N,), i32), (cu_seqlens, "cu_seqlens", (N + 1,), i32),
                  (out, "out", (Tq, H, R), dt), (lse, "lse", (Tq, H), torch.float32))
     code = _dt(q)
     if not 0 <= R <= D:
@@ -157,11 +185,128 @@ def paged_attn(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=No
     if lse is None:
         lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, 0 if workspace is not None else
-                            paged_workspace_bytes(N, Tq, H, R, D - R, page_size, max_pages, dt), dev)
-    _call("kda_mla_paged_attn", dev, _ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens),
+                            need(N, Tq, H, R, D - R, page_size, max_pages, dt), dev)
+    _call(name, dev, _ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens),
           _ptr(out), _ptr(lse), N, Tq, H, R, D - R, num_pages, page_size, max_pages, float(scale), code, _ptr(ws),
           nbytes)
     return out, lse
+
+
+def paged_attn(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=None, out=None, lse=None,
+               workspace=None):
+    """Absorbed latent attention of new tokens over the paged cache.  Without
+    cu_seqlens every sequence has one new token (q [N, H, R + Dr]); with it,
+    sequence n's are rows cu[n] .. cu[n+1]-1 of q [Tq, H, R + Dr], the last of
+    its seq_lens[n] cache rows.  Returns (o [Tq, H, R], lse [Tq, H])."""
+    return _paged("kda_mla_paged_attn", False, paged_workspace_bytes, q, cache, block_table, seq_lens, latent_dim, scale,
+                  cu_seqlens, out, lse, workspace)
+
+
+@functools.lru_cache(maxsize=256)
+def paged_fp4_workspace_bytes(N, Tq, H, R, Dr, page_size, max_pages, dtype=torch.bfloat16):
+    """Bytes of device workspace paged_attn_fp4 needs."""
+    return int(lib().kda_mla_paged_fp4_workspace_bytes(N, Tq, H, R, Dr, page_size, max_pages, _DT[dtype]))
+
+
+def paged_attn_fp4(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=None, out=None, lse=None,
+                   workspace=None):
+    """paged_attn over a 4-bit cache (cache_append_fp4), on the values that its rows stand for."""
+    return _paged("kda_mla_paged_attn_fp4", True, paged_fp4_workspace_bytes, q, cache, block_table, seq_lens, latent_dim,
+                  scale, cu_seqlens, out, lse, workspace)
+
+
+def cache_gather_fp4(cache, block_table, cu_seqlens, num_tokens, latent_dim, starts=None, out=None):
+    """Rows of a 4-bit cache as bfloat16 [num_tokens, R + Dr], sequence after sequence: row cu_seqlens[n] + i is row
+    starts[n] + i (None: i) of sequence n; one that is not in the cache is zeros.  Rows behind the last sequence are
+    left as they were.  Dr follows from the cache's row bytes."""
+    if cache.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("cache must be [num_pages, page_size, row], block_table [N, max_pages]")
+    num_pages, page_size, row = cache.shape
+    N, max_pages = block_table.shape
+    R, T = int(latent_dim), int(num_tokens)
+    Dr = next((d for d in (0, 64) if fp4_row_bytes(R, d) == row), None)
+    if Dr is None:
+        raise ValueError("no 4-bit cache of latent_dim %d has rows of %d bytes" % (R, row))
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    i32 = torch.int32
+    dev = _check(cache, (cache, "cache", None, torch.uint8), (block_table, "block_table", None, i32),
+                 (cu_seqlens, "cu_seqlens", (N + 1,), i32), (starts, "starts", (N,), i32),
+                 (out, "out", (T, R + Dr), torch.bfloat16))
+    if out is None:
+        out = torch.empty((T, R + Dr), dtype=torch.bfloat16, device=dev)
+    _call("kda_mla_cache_gather_fp4", dev, _ptr(cache), _ptr(block_table), _ptr(cu_seqlens), _ptr(starts), _ptr(out), N, T,
+          R, Dr, num_pages, page_size, max_pages, KDA_BF16)
+    return out
+
+
+def _outputs(out, shapes, dev):
+    """The given int32 outputs, and new ones in the place of those that are not."""
+    unknown = () if out is None else set(out) - set(shapes)
+    if unknown:
+        raise ValueError("unknown outputs: %s" % ", ".join(sorted(unknown)))
+    got = {n: None if out is None else out.get(n) for n in shapes}
+    return {n: torch.empty(shapes[n], dtype=torch.int32, device=dev) if t is None else t for n, t in got.items()}
+
+
+def cache_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, num_tokens, out=None, workspace=None):
+    """Pages for a step's new tokens, from lengths on the GPU (all tensors int32): sequence n has seq_lens[n] rows in
+    the cache and new_lens[n] new tokens; pages come from the end of the stack free_pages[:free_count] and are written
+    into block_table [N, max_pages].  Sequences are served in order; one whose tokens do not fit its table's row or the
+    num_tokens rows of the batch, or whose pages are not there, is refused.  Returns a dict:
+
+        cu_seqlens [N + 1]       for the calls that take the new tokens
+        positions, slots [num_tokens]  0 and -1 for tokens of refused sequences and behind the last one
+        kv_lens [N]              rows with the new ones, the attention's seq_lens; -1 for a refused sequence
+        seq_lens [N], free_count [1]   the state after the step
+
+    `out` takes preallocated ones; {"seq_lens": seq_lens, "free_count": free_count} updates the state in place, as a
+    captured step does."""
+    if block_table.dim() != 2 or new_lens.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("new_lens must be [N], block_table [N, max_pages], free_pages [num_free]")
+    N, max_pages = block_table.shape
+    T = int(num_tokens)
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    i32 = torch.int32
+    shapes = {"cu_seqlens": (N + 1,), "positions": (T,), "slots": (T,), "kv_lens": (N,), "seq_lens": (N,),
+              "free_count": (1,)}
+    dev = _check(block_table, (block_table, "block_table", None, i32), (new_lens, "new_lens", (N,), i32),
+                 (seq_lens, "seq_lens", (N,), i32), (free_pages, "free_pages", None, i32),
+                 (free_count, "free_count", (1,), i32),
+                 *((t, "out[%r]" % n, shapes[n], i32) for n, t in (out or {}).items() if n in shapes))
+    o = _outputs(out, shapes, dev)
+    ws, nbytes = _workspace(workspace, 0 if workspace is not None else _plan_bytes("plan", N), dev)
+    _call("kda_mla_cache_plan", dev, _ptr(new_lens), _ptr(seq_lens), _ptr(block_table), _ptr(free_pages),
+          _ptr(free_count), free_pages.numel(), _ptr(o["cu_seqlens"]), _ptr(o["positions"]), _ptr(o["slots"]),
+          _ptr(o["kv_lens"]), _ptr(o["seq_lens"]), _ptr(o["free_count"]), N, T, int(page_size), max_pages, _ptr(ws),
+          nbytes)
+    return o
+
+
+@functools.lru_cache(maxsize=64)
+def _plan_bytes(call, N):
+    return int(getattr(lib(), "kda_mla_cache_%s_workspace_bytes" % call)(N))
+
+
+def cache_release(finished, seq_lens, block_table, free_pages, free_count, page_size, out=None, workspace=None):
+    """The pages of the sequences with finished[n] (bool [N]) back to the end of the stack free_pages[:free_count], in
+    place.  Returns a dict: seq_lens [N], 0 for these, and free_count [1]; `out` as for cache_plan."""
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [N, max_pages], free_pages [num_free]")
+    N, max_pages = block_table.shape
+    i32 = torch.int32
+    shapes = {"seq_lens": (N,), "free_count": (1,)}
+    dev = _check(block_table, (block_table, "block_table", None, i32), (finished, "finished", (N,), torch.bool),
+                 (seq_lens, "seq_lens", (N,), i32), (free_pages, "free_pages", None, i32),
+                 (free_count, "free_count", (1,), i32),
+                 *((t, "out[%r]" % n, shapes[n], i32) for n, t in (out or {}).items() if n in shapes))
+    o = _outputs(out, shapes, dev)
+    ws, nbytes = _workspace(workspace, 0 if workspace is not None else _plan_bytes("release", N), dev)
+    _call("kda_mla_cache_release", dev, _ptr(finished), _ptr(seq_lens), _ptr(block_table), _ptr(free_pages),
+          _ptr(free_count), free_pages.numel(), _ptr(o["seq_lens"]), _ptr(o["free_count"]), N, int(page_size), max_pages,
+          _ptr(ws), nbytes)
+    return o
 
 
 def _expanded_shapes(q, kv, k_pe):

@@ -423,7 +423,7 @@ kda_status kda_short_conv_step(const void* x, const void* weight, void* conv_sta
  * form trains (forward and backward below), the absorbed form serves from a
  * paged cache of the rows [c_t ; r_t].  All of it is causal.
  *
- * Shared by the five calls: dt is KDA_BF16 (KDA_F32 and KDA_F16 return
+ * Shared by these calls: dt is KDA_BF16 (KDA_F32 and KDA_F16 return
  * KDA_ERR_UNSUPPORTED); scores, softmax statistics, sums and log-sum-exps
  * are float32.  The softmax weights, and the backward's dS, are rounded to
  * bf16 as operands of the products that sum them (a row's sum of weights and
@@ -551,6 +551,121 @@ kda_status kda_mla_attn_bwd(const void* q, const void* kv, const void* k_pe, con
                             const void* dout, void* dq, void* dkv, void* dk_pe, const int* cu_seqlens,
                             int num_seqs, int B, int T, int H, int Dn, int Dr, int Dv, float scale, kda_dtype dt,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Pages for a step's new tokens, from the requests' lengths, on the device: what
+ * kda_mla_cache_append*, kda_mla_cache_gather_fp4 and kda_mla_paged_attn* take
+ * as block_table, slots, positions, seq_lens and cu_seqlens, made without the
+ * host seeing a length (so a captured graph can hold whole steps).  Free pages
+ * are a stack: free_pages[0 .. free_count - 1], taken from its end.
+ *
+ * Sequence n has s = seq_lens[n] rows in the cache (clamped into [0, max_pages *
+ * page_size]), in the pages block_table[n][0 .. ceil(s / page_size) - 1], and
+ * a = new_lens[n] new tokens (a negative value counts as 0).  Sequences are served
+ * in order: a sequence with new tokens is refused, whole, when s + a > max_pages *
+ * page_size, when its tokens end behind T (tokens counted with those of refused
+ * sequences), or when it needs pages and those of the sequences up to it, but for
+ * the ones refused for the first two reasons, are more than there are free.
+ *
+ *   new_lens, seq_lens  device int32 [N]
+ *   block_table  device int32 [N, max_pages]: the new pages' entries are written
+ *   free_pages   device int32 [num_free], free_count device int32 [1] (clamped
+ *          into [0, num_free])
+ *   cu_seqlens   device int32 [N + 1]: prefix sums of the new tokens, clamped to T
+ *   positions, slots  device int32 [T]: of token cu_seqlens[n] + i, s + i and the
+ *          cache row block_table[n][(s + i) / page_size] * page_size + (s + i) %
+ *          page_size (-1 when the entry is negative or the row's number is not
+ *          an int).  Tokens of refused sequences, and those from cu_seqlens[N]
+ *          on: 0 and -1, as a padded batch has them.
+ *   kv_lens  device int32 [N]: s + a; -1 for a refused sequence, which the
+ *          attention takes as an empty one
+ *   seq_lens_out  device int32 [N]: s + a, or s for a refused sequence; may be
+ *          seq_lens.  free_count_out  device int32 [1]: the pages left; may be
+ *          free_count.  Other outputs must not overlap inputs or each other.
+ *   workspace  at least kda_mla_cache_plan_workspace_bytes(N) bytes; scratch.
+ * A call whose seq_lens_out and free_count_out are other arrays can be repeated
+ * with the same result.  N at most 65536, T at most 2^27, max_pages * page_size
+ * below 2^31 - 256.  With N = 0 every token is padding; N = T = 0 still writes
+ * cu_seqlens and free_count_out.  Errors: KDA_ERR_NULL, KDA_ERR_SHAPE,
+ * KDA_ERR_WORKSPACE (also when not 256-byte aligned), KDA_ERR_HIP.
+ */
+size_t kda_mla_cache_plan_workspace_bytes(int N);
+kda_status kda_mla_cache_plan(const int* new_lens, const int* seq_lens, int* block_table, const int* free_pages,
+                              const int* free_count, int num_free, int* cu_seqlens, int* positions, int* slots,
+                              int* kv_lens, int* seq_lens_out, int* free_count_out, int N, int T, int page_size,
+                              int max_pages, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The pages of finished sequences back to the free list, in the order of the
+ * sequences and of their tables: block_table[n][0 .. ceil(s / page_size) - 1] of
+ * every n with finished[n] != 0 to free_pages[free_count ..].
+ *
+ *   finished  device bytes [N];  seq_lens, block_table, free_pages, free_count as
+ *          for kda_mla_cache_plan.  What does not fit into num_free entries is
+ *          lost (it cannot be when every page is in the list or in one table).
+ *   seq_lens_out  0 for finished sequences, s for the others; may be seq_lens.
+ *   free_count_out  at most num_free; may be free_count.
+ *   workspace  at least kda_mla_cache_release_workspace_bytes(N) bytes; scratch.
+ * Sizes and errors as for kda_mla_cache_plan.
+ */
+size_t kda_mla_cache_release_workspace_bytes(int N);
+kda_status kda_mla_cache_release(const unsigned char* finished, const int* seq_lens, const int* block_table,
+                                 int* free_pages, const int* free_count, int num_free, int* seq_lens_out,
+                                 int* free_count_out, int N, int page_size, int max_pages, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* The paged latent cache in 4 bits.  A row [c ; r] of R + Dr channels is held in
+ * kda_mla_fp4_row_bytes(R, Dr) bytes:
+ *
+ *   [0, R/2)            latent codes, channel 2i in the low half of byte i: sign,
+ *                       two bits of exponent, one of fraction, for 0, 0.5, 1, 1.5,
+ *                       2, 3, 4, 6 and their negatives
+ *   [R/2, R/2 + 2 Dr)   the rotary key, bf16
+ *   then R/32 bytes     E + 127 for channels 32b .. 32b+31, which are their codes'
+ *                       values times 2^E; 255: all NaN
+ *   then zeros up to a multiple of 16
+ *
+ * (codes and scales as MXFP4 of the OCP Microscaling Formats specification 1.0).
+ * A block's E is the smallest integer with max |c| <= 7 * 2^E, held to [-125, 125];
+ * its channels divided by 2^E go to the nearest code value, ties to the even code,
+ * above 6 to 6.  A block with a NaN or an infinity becomes NaN.  The values are
+ * exact in bf16.  The latent is normalised in float64 (a rounding on the way would
+ * move values near a border by a whole step).  Returns 0 for unsupported sizes.
+ */
+size_t kda_mla_fp4_row_bytes(int R, int Dr);
+
+/* kda_mla_cache_append into a 4-bit cache: the same arguments and errors, with
+ * cache [num_pages, page_size, kda_mla_fp4_row_bytes(R, Dr)] bytes. */
+kda_status kda_mla_cache_append_fp4(const void* c_kv, const float* norm_weight, float eps, const float* rope,
+                                    int num_pos, int interleaved, const int* positions, const int* slots, void* cache,
+                                    int num_pages, int page_size, const void* q_pe, void* q, int T, int H, int R,
+                                    int Dr, kda_dtype dt, void* stream);
+
+/* Rows of a 4-bit cache as bf16 values, sequence after sequence: what the
+ * expanded form's up-projection takes when a prefix is cached already.
+ *
+ *   rows   [T, R + Dr] dt: row cu_seqlens[n] + i is row starts[n] + i of sequence
+ *          n.  One that is not in the cache (before 0 or behind max_pages *
+ *          page_size, or of a page outside [0, num_pages)) is zeros.  Rows from
+ *          cu_seqlens[N] on are left as they were.
+ *   cache, block_table  as for kda_mla_paged_attn_fp4
+ *   cu_seqlens  device int32 [N + 1], clamped into [0, T];  starts device int32
+ *          [N] or NULL (0)
+ * Sizes as for kda_mla_paged_attn, T at most 2^27, T * R at most 2^34.  N = 0 or
+ * T = 0 is a no-op.
+ */
+kda_status kda_mla_cache_gather_fp4(const void* cache, const int* block_table, const int* cu_seqlens,
+                                    const int* starts, void* rows, int N, int T, int R, int Dr, int num_pages,
+                                    int page_size, int max_pages, kda_dtype dt, void* stream);
+
+/* kda_mla_paged_attn over a 4-bit cache, on the values that its rows stand for:
+ * the same arguments, limits and errors, with cache [num_pages, page_size,
+ * kda_mla_fp4_row_bytes(R, Dr)] bytes and a workspace of at least
+ * kda_mla_paged_fp4_workspace_bytes(...) bytes. */
+size_t kda_mla_paged_fp4_workspace_bytes(int N, int Tq, int H, int R, int Dr, int page_size, int max_pages,
+                                         kda_dtype dt);
+kda_status kda_mla_paged_attn_fp4(const void* q, const void* cache, const int* block_table, const int* seq_lens,
+                                  const int* cu_seqlens, void* o, float* lse, int N, int Tq, int H, int R, int Dr,
+                                  int num_pages, int page_size, int max_pages, float scale, kda_dtype dt,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* kda_status_str(kda_status s);

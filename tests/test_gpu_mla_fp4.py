@@ -1,0 +1,655 @@
+"""The paged 4-bit latent cache and its pages on the GPU against the CPU float64 oracle.
+
+Tolerances: codes, scales, gathered latents, page tables and slots are exact.
+A rotated value: half a bf16 step plus 16 float32 half steps of its terms.  The
+attention: elementwise, the bounds of oracle/mla.py on the values that the rows
+stand for (half a bf16 step for the output and for each softmax weight, half a
+float32 step an addition).  Inputs are drawn once per case; nothing is re-drawn.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_04_amd import mla
+from oracle import mla as orc
+from oracle import mla_fp4 as orc4
+
+from ._fp4_cases import in_fp4, lengths, pages
+from ._paged_cases import marked
+from .test_gpu_mla import BF16, CANARY, LATENT, _cuda, _i32, _paged, _randn, _within
+
+pytestmark = pytest.mark.gpu
+
+STATE = ("seq_lens", "free_count")
+
+
+def _same(tag, got, want):
+    for n, w in want.items():
+        assert np.array_equal(got[n].cpu().numpy(), np.asarray(w)), (tag, n, got[n].cpu().numpy(), np.asarray(w))
+
+
+# ---------------------------------------------------------------------------
+# pages
+# ---------------------------------------------------------------------------
+def _check_plan(tag, new, lens, table, free, count, page, T, in_place=False):
+    want = orc4.plan(new, lens, table, free, int(count[0]), page, T)
+    args = _cuda(_i32(new), _i32(lens), _i32(table), _i32(free), _i32(count))
+    out = {"positions": torch.full((T,), 55, dtype=torch.int32, device="cuda")}
+    if in_place:
+        out |= {"seq_lens": args[1], "free_count": args[4]}
+    got = mla.cache_plan(*args, page, T, out=out)
+    _same(tag, got | {"block_table": args[2]}, want)
+    assert np.array_equal(args[3].cpu().numpy(), free)
+    if in_place:
+        assert got["seq_lens"] is args[1] and got["free_count"] is args[4]
+    else:
+        _same(tag, {"seq_lens": args[1], "free_count": args[4]}, {"seq_lens": lens, "free_count": count})
+    return want
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 64])
+@pytest.mark.parametrize("N,hi", [(1, 1), (1, 40), (2, 700), (63, 1), (65, 30), (300, 9), (1500, 3)])
+def test_plan(page, N, hi):
+    print("CASE plan", N, hi, page, flush=True)
+    per = max(1, -(-(2 * hi + 20) // page))
+    lens, table, free, count = pages(N + page, N, per, page)
+    lens = np.minimum(lens, per * page - 5)  # some sequences fill their row and are refused
+    new = lengths(N + 7, N, hi)
+    total = int(new.sum())
+    for T in {total, total + 5, max(total - 3, 0)}:
+        _check_plan("all pages", new, lens, table, free, count, page, T)
+        for few in (0, 1, int(count[0]) // 3):
+            _check_plan("few pages", new, lens, table, free, np.array([few], np.int32), page, T, in_place=True)
+
+
+def test_plan_of_numbers_out_of_range():
+    """Negative and huge lengths and counts: held to their range, and no access leaves the buffers."""
+    lens, table, free, count = pages(3, 9, 4, 8)
+    new = np.array([3, -4, 1 << 30, 2, 0, 1, 40, 5, 2147483647], np.int32)
+    lens = np.array([-7, 5, 0, 1 << 30, 2147483647, 31, 0, -2147483648, 3], np.int32)
+    for c in (-5, 3, 1 << 30):
+        free[:] = np.arange(len(free))
+        _check_plan("range", new, lens, table, free, np.array([c], np.int32), 8, 50)
+    table[:, 0] = -1            # a sequence whose pages are not there gets no slots in them
+    _check_plan("no page", np.full(9, 2, np.int32), np.full(9, 1, np.int32), table, free, count, 8, 18)
+    table[:, 0] = (1 << 31) // 8 - 1
+    table[3, 0] += 1            # its rows' numbers are no ints
+    _check_plan("far page", np.full(9, 2, np.int32), np.full(9, 1, np.int32), table, free, count, 8, 18)
+
+
+def test_plan_of_nothing():
+    e = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = mla.cache_plan(e(0), e(0), e(0, 4), e(3), e(1) + 2, 16, 5)
+    _same("none", got, dict(cu_seqlens=[0], positions=[0] * 5, slots=[-1] * 5, kv_lens=[], seq_lens=[], free_count=[2]))
+    got = mla.cache_plan(e(2), e(2), e(2, 4), e(0), e(1), 16, 0)
+    _same("none", got, dict(cu_seqlens=[0] * 3, positions=[], slots=[], kv_lens=[0] * 2, seq_lens=[0] * 2, free_count=[0]))
+    got = mla.cache_plan(e(2) + 1, e(2), e(2, 0), e(0), e(1), 16, 2)
+    _same("none", got, dict(cu_seqlens=[0, 1, 2], slots=[-1] * 2, kv_lens=[-1] * 2, seq_lens=[0] * 2, free_count=[0]))
+
+
+@pytest.mark.parametrize("N,T", [(1 << 16, 1 << 16), (1 << 16, 900), (5, 200000), (3000, 50000)])
+def test_plan_of_large_batches(N, T):
+    print("CASE plan", N, T, flush=True)
+    r = np.random.default_rng(N)
+    new = np.bincount(r.integers(0, N, T - T // 50), minlength=N).astype(np.int32)
+    page, per = 16, int(new.max()) // 16 + 3
+    lens = r.integers(0, 33, N).astype(np.int32)
+    table = r.permutation(N * per).reshape(N, per).astype(np.int32)
+    free = r.permutation(int(new.sum()) + N).astype(np.int32)
+    _check_plan("large", new, lens, table, free, np.array([len(free) // 2], np.int32), page, T)
+
+
+@pytest.mark.parametrize("N,per,page", [(1, 1, 1), (5, 3, 16), (70, 30, 4), (300, 200, 16), (2000, 4, 64), (1 << 16, 2, 1)])
+def test_release(N, per, page):
+    print("CASE release", N, per, page, flush=True)
+    lens, table, free, count = pages(N + per, N, per, page)
+    r = np.random.default_rng(N)
+    for share in (0.0, 0.3, 1.0):
+        done = r.random(N) < share
+        for in_place, stack in ((False, free), (True, free[:int(count[0]) + int(lens.sum()) // (3 * page)])):
+            want = orc4.release(done, lens, table, stack, int(count[0]), page)
+            args = _cuda(torch.tensor(done), _i32(lens), _i32(table), _i32(stack), _i32(count))
+            out = {"seq_lens": args[1], "free_count": args[4]} if in_place else None
+            got = mla.cache_release(*args, page, out=out)
+            _same("release", got | {"free_pages": args[3]}, want)
+            assert np.array_equal(args[2].cpu().numpy(), table)
+
+
+# ---------------------------------------------------------------------------
+# append, gather
+# ---------------------------------------------------------------------------
+def _rope(n_pos, Dr):
+    ang = np.arange(n_pos)[:, None] * 100.0 ** (-np.arange(Dr // 2) / max(Dr // 2, 1))
+    return torch.tensor(np.concatenate([np.cos(ang), np.sin(ang)], 1), dtype=torch.float32)
+
+
+def _parts(rows, R, Dr):
+    """Codes, key values and scales of rows [n, W]; the bytes behind them."""
+    rows = rows.numpy()
+    lo, hi = rows[:, :R // 2] & 15, rows[:, :R // 2] >> 4
+    pe = np.ascontiguousarray(rows[:, R // 2:R // 2 + 2 * Dr]).view("<u2").astype(np.uint32) << 16
+    at = R // 2 + 2 * Dr
+    return (np.stack([lo, hi], -1).reshape(len(rows), R), pe.view(np.float32), rows[:, at:at + R // 32],
+            rows[:, at + R // 32:])
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+@pytest.mark.parametrize("T", [1, 7, 130])
+def test_append_fp4(R, Dr, T):
+    print("CASE append", R, Dr, T, flush=True)
+    r = np.random.default_rng(T)
+    P, page, H, n_pos = 9, 24, 5, 300
+    rope, W = _rope(n_pos, Dr), orc4.row_bytes(R, Dr)
+    assert mla.fp4_row_bytes(R, Dr) == W
+    c, q_pe, q0 = _randn(T, T, R + Dr), _randn(T + 1, T, H, Dr), _randn(T + 2, T, H, R + Dr)
+    c[::3, :R] *= torch.exp2(torch.linspace(-9, 9, R)).to(BF16)  # blocks of different sizes
+    c[T // 2, 32:64] = 0
+    w = 1 + 0.3 * torch.randn(R, generator=torch.Generator().manual_seed(T))
+    pos = r.integers(-5, n_pos + 5, T).astype(np.int32)
+    slots = r.permutation(P * page)[:T].astype(np.int32)
+    slots[::4] = r.choice([-1, P * page, 1 << 30], len(slots[::4]))
+    if T == 1:
+        slots[0] = 5
+    for inter, use_w, use_rope in ((False, True, Dr > 0), (True, False, Dr > 0), (False, True, False)):
+        cache0 = torch.from_numpy(r.integers(0, 256, (P, page, W)).astype(np.uint8))
+        cache, q = cache0.cuda(), q0.cuda()
+        got = mla.cache_append_fp4(c.cuda(), _i32(pos).cuda(), _i32(slots).cuda(), cache, R,
+                                   rope=rope.cuda() if use_rope else None, norm_weight=w.cuda() if use_w else None,
+                                   eps=2.0 ** -17, interleaved=inter, q_pe=q_pe.cuda() if Dr else None, q=q if Dr else None)
+        assert got is cache
+        codes, scales, pe, qr = orc4.append_rows(c, R, rope=rope if use_rope else None, positions=pos,
+                                                 norm_weight=w if use_w else None, eps=2.0 ** -17, interleaved=inter,
+                                                 q_pe=q_pe if Dr else None)
+        flat = cache.cpu().view(P * page, W)
+        kept = (slots >= 0) & (slots < P * page)
+        gc, gp, gs, rest = _parts(flat[torch.as_tensor(slots[kept]).long()], R, Dr)
+        assert np.array_equal(gs, scales[kept]) and np.array_equal(gc, codes[kept]) and not rest.any()
+        if Dr:
+            mag = np.abs(c.double().numpy()[:, R:]).max() * np.ones(pe.shape)
+            _within("key", torch.from_numpy(gp), pe[kept], (orc.E * np.abs(pe) + 16 * orc.U * mag)[kept])
+            qmag = np.abs(q_pe.double().numpy()).max() * np.ones(q_pe.shape)
+            assert torch.equal(q.cpu()[..., :R], q0[..., :R])
+            _within("q", q[..., R:], qr, orc.E * np.abs(qr) + 16 * orc.U * qmag)
+        others = torch.as_tensor(np.setdiff1d(np.arange(P * page), slots[kept]))
+        assert torch.equal(flat[others], cache0.view(P * page, W)[others])
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_append_fp4_ties_limits_and_non_finite_values(R, Dr):
+    """Values that lie on the codes' borders, blocks of one value, the largest and smallest numbers, infinities, NaN."""
+    T = 8
+    r = np.random.default_rng(R + Dr)
+    c = torch.zeros(T, R + Dr, dtype=BF16)
+    ties = torch.tensor([6.0, 0.25, -0.75, 1.25, -1.75, 2.5, -3.5, 5.0, 7.0, -5.0, 3.5, -2.5, 1.75, -1.25, 0.75, -0.25])
+    c[0, :R] = ties.repeat(R // 16) * 2.0 ** r.integers(-30, 30)
+    c[1, :R] = ties[r.integers(1, 16, R)] * 2.0 ** -7
+    c[2, :R] = torch.tensor(r.standard_normal(R)) * 2.0 ** 120
+    c[2, :64] = torch.finfo(BF16).max
+    c[3, :R] = torch.tensor(r.standard_normal(R)) * 2.0 ** -126
+    c[3, 40] = 2.0 ** -133
+    c[4, :R] = torch.tensor(r.standard_normal(R))
+    c[4, 7], c[4, 50], c[4, R - 1] = float("inf"), float("nan"), float("-inf")
+    c[5, :R:32] = 7.0
+    c[6, :R:32] = 7.0625
+    c[7, :] = -0.0
+    W = orc4.row_bytes(R, Dr)
+    cache = torch.full((1, 16, W), 255, dtype=torch.uint8, device="cuda")
+    mla.cache_append_fp4(c.cuda(), None, _i32(np.arange(T) * 2).cuda(), cache, R)
+    gc, _, gs, rest = _parts(cache.cpu()[0, 0:16:2], R, Dr)
+    codes, scales = orc4.quantise(c[:, :R])
+    assert np.array_equal(gs, scales) and np.array_equal(gc, codes) and not rest.any()
+    assert (gs[4] == 255).sum() == (3 if R > 64 else 2)
+    # with the norm, a row with a value that is not finite is NaN as a whole; a row of zeros stays zeros
+    w = torch.ones(R)
+    mla.cache_append_fp4(c[4:8].cuda(), None, _i32([0, 2, 4, 6]).cuda(), cache, R, norm_weight=w.cuda())
+    gc, _, gs, _ = _parts(cache.cpu()[0, 0:8:2], R, Dr)
+    assert (gs[0] == 255).all() and (gs[3] == 2).all() and not (gc[3] & 7).any() and (gs[1:3] != 255).all()
+
+
+def _gather_want(vals, table, cu, starts, T):
+    num_pages, page, D = vals.shape
+    want = np.full((T, D), CANARY)
+    for n in range(len(cu) - 1):
+        for t in range(cu[n], cu[n + 1]):
+            j = int(t) - int(cu[n]) + (0 if starts is None else int(starts[n]))
+            want[t] = 0.0
+            if 0 <= j < table.shape[1] * page and 0 <= table[n][j // page] < num_pages:
+                want[t] = vals[table[n][j // page], j % page]
+    return want
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+@pytest.mark.parametrize("page", [1, 24, 64])
+def test_gather(R, Dr, page):
+    print("CASE gather", R, Dr, page, flush=True)
+    r = np.random.default_rng(page)
+    rows, vals = in_fp4(_randn(page, 23, page, R + Dr), R)
+    N, per = 5, max(2, 100 // page)
+    table = r.integers(0, 23, (N, per)).astype(np.int32)
+    table[1, 0], table[2, -1], table[3, 1] = -1, 23, 1 << 30
+    cu = np.array([0, 0, 40, 41, 90, 100], np.int32)
+    for starts in (None, np.array([5, -3, per * page - 1, 2147483647, 7], np.int32)):
+        out = torch.full((107, R + Dr), CANARY, dtype=BF16, device="cuda")
+        got = mla.cache_gather_fp4(*_cuda(rows, _i32(table), _i32(cu)), 107, R,
+                                   starts=None if starts is None else _i32(starts).cuda(), out=out)
+        assert got is out
+        assert np.array_equal(got.cpu().double().numpy(), _gather_want(vals, table, cu, starts, 107))
+    empty = torch.empty((0, page, orc4.row_bytes(R, Dr)), dtype=torch.uint8, device="cuda")
+    got = mla.cache_gather_fp4(empty, *_cuda(_i32(table), _i32(cu)), 100, R)
+    assert not got.any()
+    assert mla.cache_gather_fp4(*_cuda(rows, _i32(table), _i32(cu)), 0, R).shape == (0, R + Dr)
+
+
+def test_gather_many_sequences_and_clamped_ends():
+    rows, vals = in_fp4(_randn(9, 50, 4, 192), 128)
+    r = np.random.default_rng(5)
+    lens = r.integers(0, 9, 700)
+    table = r.integers(0, 50, (700, 2)).astype(np.int32)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1]) - 40
+    got = mla.cache_gather_fp4(*_cuda(rows, _i32(table), _i32(cu)), T, 128)
+    assert np.array_equal(got.cpu().double().numpy(), _gather_want(vals, table, np.minimum(cu, T), None, T))
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+def _check_paged(tag, q, cache, table, lens, cu, R, scale=None):
+    scale = (128 + q.shape[-1] - R) ** -0.5 if scale is None else scale
+    Tq, H, D = q.shape
+    rows, vals = in_fp4(cache, R)
+    dev = _cuda(q, rows, _i32(table), _i32(lens), None if cu is None else _i32(cu))
+    o = torch.full((Tq, H, R), CANARY, dtype=BF16, device="cuda")
+    lse = torch.full((Tq, H), CANARY, device="cuda")
+    need = mla.paged_fp4_workspace_bytes(len(lens), Tq, H, R, D - R, cache.shape[1], table.shape[1])
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    mla.paged_attn_fp4(*dev[:4], R, scale, cu_seqlens=dev[4], out=o, lse=lse, workspace=ws[:need] if need else None)
+    torch.cuda.synchronize()
+    assert bool((ws[need:] == 255).all())
+    r = orc.paged_attention(q, vals, table, lens, R, scale, cu_seqlens=cu)
+    _within(tag + " o", o, r[0], r[2])
+    _within(tag + " lse", lse, r[1], r[3])
+    if cu is not None and cu[-1] < Tq:
+        assert bool((o[cu[-1]:] == CANARY).all()) and bool((lse[cu[-1]:] == CANARY).all())
+    return o, lse
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+@pytest.mark.parametrize("page", [1, 16, 24, 64, 100])
+def test_paged_fp4_single_tokens(R, Dr, page):
+    print("CASE paged", R, Dr, page, flush=True)
+    _check_paged("page %d" % page, *_paged(page, [1, 31, 32, 33, 63, 64, 65, 0, 96, 97, 300], page, 5, R, Dr), R)
+
+
+@pytest.mark.parametrize("H", [1, 8, 16, 31, 32, 33, 64, 65, 96, 97, 100, 128, 129, 200])
+@pytest.mark.parametrize("R,Dr", [(128, 0), (256, 64), (512, 64)])
+def test_paged_fp4_heads(H, R, Dr):
+    print("CASE heads", H, R, flush=True)
+    _check_paged("H %d" % H, *_paged(H, [70, 131], 16, H, R, Dr), R)
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_chunks(R, Dr):
+    """New tokens that end a longer cache, fill it, outnumber it (rows that see nothing), or are none; padding behind."""
+    print("CASE chunks", R, Dr, flush=True)
+    _check_paged("chunks", *_paged(5, [200, 70, 9, 40, 0], 24, 3, R, Dr, q_lens=[50, 70, 20, 0, 6], pad=11), R)
+    _check_paged("chunks", *_paged(6, [129, 33, 1], 16, 12, R, Dr, q_lens=[17, 33, 1]), R)
+
+
+def test_paged_fp4_chunk_spans_many_row_blocks():
+    _check_paged("long chunk", *_paged(6, [150, 260], 64, 12, 512, 64, q_lens=[150, 33]), 512)
+
+
+def test_paged_fp4_long_cache_is_split():
+    _check_paged("long", *_paged(9, [20000], 64, 8, 128, 64), 128)
+    _check_paged("long ragged", *_paged(10, [9000, 3, 0, 2500], 64, 4, 512, 64), 512)
+
+
+def _check_all_rows(tag, q, cache, table, lens, cu, R, scale):
+    """Every row of a large call against float64 on the GPU, within the bounds of oracle.mla.attend."""
+    Tq, H, D = q.shape
+    rows, vals = in_fp4(cache, R)
+    dq, dc, dt, dl = _cuda(q, rows, _i32(table), _i32(lens))
+    vals = torch.from_numpy(vals).cuda()
+    o, lse = mla.paged_attn_fp4(dq, dc, dt, dl, R, scale, cu_seqlens=None if cu is None else _i32(cu).cuda())
+    torch.cuda.synchronize()
+    print("DONE", tag, flush=True)
+    starts = np.arange(len(lens) + 1) if cu is None else cu
+    worst = [0.0, 0.0]
+    for n, L in enumerate(lens):
+        b, e, L = int(starts[n]), int(starts[n + 1]), int(L)
+        if e == b:
+            continue
+        j = torch.arange(L, device="cuda")
+        page = dt[n].long()[j // cache.shape[1]]
+        there = (page >= 0) & (page < cache.shape[0])
+        k = vals[page.clamp(0, cache.shape[0] - 1), j % cache.shape[1]] * there[:, None]
+        qq = dq[b:e].double().reshape(-1, D)
+        tok = torch.arange(e - b, device="cuda").repeat_interleave(H)
+        sees = there & (j <= (L - (e - b) + tok)[:, None])
+        s = (qq @ k.T * scale).masked_fill(~sees, -float("inf"))
+        es = ((D + 16) * orc.U * scale * (qq.abs() @ k.abs().T)).masked_fill(~sees, 0.0)
+        lse64 = torch.logsumexp(s, -1) if L else torch.full((len(qq),), -float("inf"), device="cuda").double()
+        empty = torch.isinf(lse64)
+        p = torch.exp(s - lse64.masked_fill(empty, 0.0)[:, None])
+        want, mag = p @ k[:, :R], p @ k[:, :R].abs()
+        w = es.amax(-1, keepdim=True) if L else es.sum(-1, keepdim=True)
+        err = (orc.E + 2 * w + (64 + L) * orc.U) * mag + orc.E * want.abs()
+        err_l = w[:, 0] + (64 + L) * orc.U + 4 * orc.U * lse64.masked_fill(empty, 0.0).abs()
+        got, got_l = o[b:e].double().reshape(-1, R), lse[b:e].double().reshape(-1)
+        assert bool((got_l[empty] == -float("inf")).all()) and bool((got[empty] == 0).all()), (tag, n)
+        off, off_l = (got - want).abs(), (got_l - lse64)[~empty].abs()
+        assert bool((off <= err + 1e-30).all()) and bool((off_l <= err_l[~empty]).all()), (tag, n, float((off / (err + 1e-30)).max()))
+        worst = [max(worst[0], float((off / (err + 1e-30)).max())), max([worst[1], *(off_l / err_l[~empty]).tolist()])]
+    print("BOUND %-28s of its bound at most %.2f, lse %.2f" % (tag, *worst), flush=True)
+
+
+def _many(R, seed, hi=6000):
+    """Lengths whose tiles are many times the workgroups', short and empty sequences among them."""
+    lens = np.random.default_rng(seed).integers(1, hi + 1, 420 if R == 128 else 220)
+    lens[3::17] = lens[3::17] % 200
+    lens[5], lens[40] = 0, hi
+    return lens
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+@pytest.mark.parametrize("H,page", [(5, 16), (40, 64), (96, 100)])
+def test_paged_fp4_long_runs_of_tiles(R, Dr, H, page):
+    """Runs of many tiles a workgroup, over the ends of sequences, in each height of blocks."""
+    print("CASE runs", R, Dr, H, page, flush=True)
+    _check_all_rows("runs H%d R%d" % (H, R), *marked(H + R, _many(R, H), page, H, R, Dr, pool=9), R, 0.1)
+
+
+@pytest.mark.parametrize("H", [5, 40, 96])
+def test_paged_fp4_long_runs_with_missing_pages(H):
+    print("CASE runs, missing", H, flush=True)
+    q, cache, table, lens, cu = marked(71 + H, _many(512, H + 1), 24, H, 512, 64, pool=9)
+    r = np.random.default_rng(H)
+    gone = r.random(table.shape) < 0.03
+    table[gone] = r.choice([-1, cache.shape[0], 1 << 30], int(gone.sum()))
+    _check_all_rows("missing H%d" % H, q, cache, table, lens, cu, 512, 0.1)
+
+
+@pytest.mark.parametrize("R,Dr,H", [(512, 64, 5), (512, 0, 40), (512, 64, 96), (256, 64, 12), (128, 0, 8), (128, 64, 96)])
+def test_paged_fp4_long_runs_of_rising_scores(R, Dr, H):
+    print("CASE runs, rising", R, Dr, H, flush=True)
+    _check_all_rows("rising H%d R%d" % (H, R), *marked(81 + H, _many(R, H + 2), 64, H, R, Dr, pool=9, rise=(0.05, 4.0)), R, 0.3)
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_long_runs_of_chunks(R, Dr):
+    """Several row blocks a sequence, each a run of tiles or more."""
+    print("CASE runs, chunks", R, Dr, flush=True)
+    r = np.random.default_rng(R + Dr)
+    N = 48 if R == 128 else 24
+    q_lens = r.integers(0, 90, N)
+    lens = np.maximum(r.integers(1500, 6000, N), q_lens)
+    lens[2], lens[7] = q_lens[2], q_lens[7] // 2  # a first chunk, and one with rows that see nothing
+    _check_all_rows("chunks R%d" % R, *marked(91 + R, lens, 24, 16, R, Dr, q_lens=q_lens, pool=9), R, 0.1)
+
+
+@pytest.mark.parametrize("R,Dr,H,lens", [(128, 0, 8, [20000]), (512, 64, 12, [131072]), (256, 0, 64, [70000, 900]),
+                                         (512, 64, 96, [30000, 0, 41000])])
+def test_paged_fp4_every_part_of_a_long_cache(R, Dr, H, lens):
+    print("CASE parts", R, H, lens, flush=True)
+    _check_all_rows("parts R%d" % R, *marked(101 + H, lens, 64, H, R, Dr, pool=3), R, 0.1)
+
+
+@pytest.mark.parametrize("R,Dr,H", [(256, 64, 16), (512, 64, 96), (128, 0, 40)])
+def test_paged_fp4_scores_that_rise_and_large_ones(R, Dr, H):
+    q, cache, table, lens, cu = _paged(12, [700], 16, H, R, Dr)
+    up = torch.linspace(0.05, 4.0, 700)
+    for j in range(700):
+        cache[table[0][j // 16], j % 16] = (cache[table[0][j // 16], j % 16].float() * up[j]).to(BF16)
+    _check_paged("rising", q, cache, table, lens, cu, R, scale=0.7)
+
+
+def test_paged_fp4_scales_far_apart():
+    """Blocks of 2^-60 to 2^40 in one row, the queries the other way round, so that every block counts in a score."""
+    R, Dr = 512, 64
+    q, cache, table, lens, cu = _paged(17, [150, 40], 16, 9, R, Dr)
+    up = torch.exp2(torch.linspace(-60, 40, R // 32).round()).repeat_interleave(32)
+    cache[..., :R] = (cache[..., :R].float() * up).to(BF16)
+    q[..., :R] = (q[..., :R].float() / up).to(BF16)
+    _check_paged("far apart", q, cache, table, lens, cu, R)
+
+
+def test_paged_fp4_missing_pages_are_left_out():
+    q, cache, table, lens, cu = _paged(13, [200, 130, 64], 16, 9, 128, 64)
+    table[0][[0, 3, 7]] = [-1, 1 << 30, cache.shape[0]]
+    table[1][:] = -5                       # nothing is there: a row that sees nothing
+    _check_paged("missing", q, cache, table, lens, cu, 128)
+
+
+def test_paged_fp4_lengths_are_clamped_and_pages_shared():
+    q, cache, table, lens, cu = _paged(14, [48, 48], 16, 4, 128, 0)
+    table = table[:, :3].copy()
+    table[1] = table[0]                    # a shared prefix
+    _check_paged("clamped", q, cache, table, np.array([1 << 30, -7], np.int32), cu, 128)
+
+
+@pytest.mark.parametrize("R,Dr,H", [(512, 64, 8), (128, 0, 40), (256, 64, 96)])
+def test_paged_fp4_rows_of_other_sequences_do_not_matter(R, Dr, H):
+    q, cache, table, lens, cu = _paged(15, [100, 90, 300], 16, H, R, Dr)
+    rows, _ = in_fp4(cache, R)
+    args = lambda: (*_cuda(q, rows, _i32(table), _i32(lens)), R, 0.07)  # noqa: E731
+    o, lse = mla.paged_attn_fp4(*args())
+    for j in range(90):
+        rows[table[1][j // 16], j % 16] = 255
+    o2, lse2 = mla.paged_attn_fp4(*args())
+    keep = torch.tensor([0, 2], device="cuda")
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+    assert bool(torch.isnan(o2[1].float()).all())
+
+
+def test_paged_fp4_many_sequences():
+    """More sequences than threads of a workgroup: single tokens, and chunks with empty ones among them."""
+    r = np.random.default_rng(23)
+    lens = r.integers(0, 90, 700).tolist()
+    _check_paged("700 single", *_paged(23, lens, 16, 2, 128, 64), 128)
+    _check_paged("700 chunks", *_paged(24, lens, 16, 2, 128, 0, q_lens=r.integers(0, 4, 700).tolist(), pad=3), 128)
+
+
+@pytest.mark.parametrize("R,Dr,H", [(128, 64, 1), (512, 0, 80)])
+def test_paged_fp4_most_sequences(R, Dr, H):
+    """65,536 sequences of one cache row or none (with 80 heads of 512 channels, offsets of q and o past 2^31): a row
+    that sees one row gives its latent, exactly."""
+    print("CASE most sequences", R, H, flush=True)
+    N, n_pages, page = 1 << 16, 300, 4
+    g = torch.Generator(device="cuda").manual_seed(R)
+    rows, vals = in_fp4(_randn(R, n_pages, page, R + Dr), R)
+    rows, vals = rows.cuda(), torch.from_numpy(vals).cuda().to(BF16)
+    table = torch.randint(0, n_pages, (N, 2), generator=g, device="cuda", dtype=torch.int32)
+    lens = (torch.rand(N, generator=g, device="cuda") < 0.8).to(torch.int32)
+    q = torch.randn((N, H, R + Dr), generator=g, device="cuda", dtype=BF16)
+    o, lse = mla.paged_attn_fp4(q, rows, table, lens, R, 0.05)
+    for b in range(0, N, 4096):
+        x = slice(b, b + 4096)
+        one = lens[x, None, None] == 1
+        row = vals[table[x, 0].long(), 0]
+        assert torch.equal(o[x], torch.where(one, row[:, None, :R], torch.zeros((), dtype=BF16, device="cuda")).expand(-1, H, -1))
+        s = (q[x].float() * row[:, None].float()).sum(-1) * 0.05
+        mag = (q[x].float() * row[:, None].float()).abs().sum(-1) * 0.05
+        off = (lse[x] - s).abs() - (2 * (R + Dr + 16) * orc.U * mag + 64 * orc.U)  # two float32 sums
+        assert bool((torch.where(one[..., 0], off, -torch.ones_like(off)) <= 0).all())
+        assert bool(torch.isneginf(lse[x][lens[x] == 0]).all())
+
+
+def test_paged_fp4_most_heads():
+    _check_paged("H 1024", *_paged(25, [130], 64, 1024, 256, 0), 256)
+
+
+def test_paged_fp4_no_pages_and_no_rows():
+    q = _randn(26, 3, 4, 192).cuda()
+    empty = torch.empty((0, 16, orc4.row_bytes(128, 64)), dtype=torch.uint8, device="cuda")
+    for per in (0, 2):  # a table that names pages of an empty cache, and none
+        table = torch.zeros((3, per), dtype=torch.int32, device="cuda")
+        o, lse = mla.paged_attn_fp4(q, empty, table, _i32([0, 5, 9]).cuda(), 128, 0.1)
+        assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    o, lse = mla.paged_attn_fp4(q[:0], empty, table[:0], _i32([]).cuda(), 128, 0.1)
+    assert o.shape == (0, 4, 128)
+
+
+def test_fp4_offsets_past_32_bits():
+    """Rows past 2^32 bytes of the cache: appended, gathered, attended."""
+    page, R, Dr = 64, 512, 64
+    W = orc4.row_bytes(R, Dr)
+    n_pages = (1 << 32) // (page * W) + 40
+    cache = torch.zeros((n_pages, page, W), dtype=torch.uint8, device="cuda")
+    table = np.array([[n_pages - 1, 3, n_pages - 7]], np.int32)
+    c = _randn(16, 150, R + Dr)
+    slots = np.array([int(table[0][j // page]) * page + j % page for j in range(150)], np.int32)
+    mla.cache_append_fp4(c.cuda(), None, _i32(slots).cuda(), cache, R)
+    rows, vals = in_fp4(torch.cat([c, torch.zeros(42, R + Dr, dtype=BF16)]).view(3, page, -1), R)
+    got = mla.cache_gather_fp4(cache, _i32(table).cuda(), _i32([0, 150]).cuda(), 150, R)
+    assert np.array_equal(got.cpu().double().numpy(), vals.reshape(192, -1)[:150])
+    q = _randn(17, 1, 12, R + Dr)
+    o, lse = mla.paged_attn_fp4(q.cuda(), cache, _i32(table).cuda(), _i32([150]).cuda(), R, 0.07)
+    r = orc.paged_attention(q, vals, np.array([[0, 1, 2]]), [150], R, 0.07)
+    _within("far o", o, r[0], r[2])
+    _within("far lse", lse, r[1], r[3])
+
+
+def test_fp4_calls_without_a_log_sum_exp_repeat_bitwise():
+    ptr = lambda t: t.data_ptr()  # noqa: E731
+    q, cache, table, lens, _ = _paged(72, [300, 20000], 64, 5, 128, 64)
+    q, rows, table, lens = _cuda(q, in_fp4(cache, 128)[0], _i32(table), _i32(lens))
+    o, lse = mla.paged_attn_fp4(q, rows, table, lens, 128, 0.1)
+    again = mla.paged_attn_fp4(q, rows, table, lens, 128, 0.1)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    need = mla.paged_fp4_workspace_bytes(2, 2, 5, 128, 64, 64, table.shape[1])
+    got, ws = torch.empty_like(o), torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    assert mla.lib().kda_mla_paged_attn_fp4(ptr(q), ptr(rows), ptr(table), ptr(lens), None, ptr(got), None, 2, 2, 5, 128, 64,
+                                            rows.shape[0], 64, table.shape[1], 0.1, mla.KDA_BF16, ptr(ws), need,
+                                            torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(o, got)
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+class Loop:
+    """A serving loop's state and its step: pages, append, attention; then finished sequences give their pages back."""
+
+    def __init__(self, R=512, Dr=64, H=8, N=6, per=5, page=16, pages=12, T=64):
+        self.R, self.H, self.N, self.page, self.T, self.D = R, H, N, page, T, R + Dr
+        i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.new, self.lens, self.table = i32(N), i32(N), i32(N, per) - 1
+        self.free, self.count = torch.arange(pages, dtype=torch.int32, device="cuda"), i32(1) + pages
+        self.cache = torch.full((pages, page, mla.fp4_row_bytes(R, Dr)), 255, dtype=torch.uint8, device="cuda")
+        self.done = torch.zeros(N, dtype=torch.bool, device="cuda")
+        self.c = torch.zeros(T, self.D, dtype=BF16, device="cuda")
+        self.q = torch.zeros(T, H, self.D, dtype=BF16, device="cuda")
+        self.w = 1 + 0.1 * torch.randn(R, generator=torch.Generator().manual_seed(3)).cuda()
+
+    def state(self):
+        return [self.lens, self.table, self.free, self.count, self.cache]
+
+    def step(self):
+        p = mla.cache_plan(self.new, self.lens, self.table, self.free, self.count, self.page, self.T,
+                           out={"seq_lens": self.lens, "free_count": self.count})
+        mla.cache_append_fp4(self.c, p["positions"], p["slots"], self.cache, self.R, norm_weight=self.w)
+        o, lse = torch.zeros_like(self.q[..., :self.R]).contiguous(), torch.zeros(self.T, self.H, device="cuda")
+        mla.paged_attn_fp4(self.q, self.cache, self.table, p["kv_lens"], self.R, 0.07, cu_seqlens=p["cu_seqlens"], out=o, lse=lse)
+        mla.cache_release(self.done, self.lens, self.table, self.free, self.count, self.page,
+                          out={"seq_lens": self.lens, "free_count": self.count})
+        return o, lse, p["kv_lens"], p["cu_seqlens"]
+
+
+def test_a_serving_loop_in_a_graph():
+    """Steps of a loop (prompts, single tokens, refusals, ends), eager and replayed, against the oracle on the values
+    that each sequence's own tokens were held as."""
+    r = np.random.default_rng(8)
+    loop, twin = Loop(), Loop()
+    for _ in range(2):  # warm, on a state that is put back
+        loop.step()
+    fresh = Loop()
+    for a, b in zip(loop.state(), fresh.state()):
+        a.copy_(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = loop.step()
+    for a, b in zip(loop.state(), fresh.state()):
+        a.copy_(b)
+    N, T, R, H = loop.N, loop.T, loop.R, loop.H
+    held = [np.zeros((0, loop.D)) for _ in range(N)]
+    refused = 0
+    for step in range(14):
+        new = np.where(r.random(N) < 0.4, r.integers(0, 19, N), 1)
+        while new.sum() > T - 2:
+            new = new // 2
+        done = r.random(N) < 0.15
+        c, q = _randn(100 + step, T, loop.D), _randn(200 + step, T, H, loop.D)
+        for x in (loop, twin):
+            x.new.copy_(_i32(new)), x.done.copy_(torch.tensor(done)), x.c.copy_(c), x.q.copy_(q)
+        for t in outs:
+            t.fill_(7)
+        graph.replay()
+        eager = twin.step()
+        torch.cuda.synchronize()
+        for a, b in zip([*outs, *loop.state()], [*eager, *twin.state()]):
+            assert torch.equal(a, b), step
+        o, lse, kv, cu = (t.cpu() for t in outs)
+        codes, scales, pe, _ = orc4.append_rows(c, R, norm_weight=loop.w.cpu())
+        rows = np.concatenate([orc4.values(codes, scales), pe], -1)
+        for n in range(N):
+            b, e = int(cu[n]), int(cu[n + 1])
+            assert e - b == new[n]
+            if kv[n] < 0:
+                refused += 1
+                assert bool((o[b:e] == 0).all()) and bool(torch.isneginf(lse[b:e]).all())
+                continue
+            held[n] = np.concatenate([held[n], rows[b:e]])
+            assert kv[n] == len(held[n])
+            for h in range(H):
+                want = orc.attend(q[b:e, h].double().numpy(), held[n], held[n][:, :R], len(held[n]) - (e - b), 0.07)
+                _within("step %d" % step, o[b:e, h], want[0], want[2])
+                _within("step %d lse" % step, lse[b:e, h], want[1], want[3])
+        assert bool((o[cu[N]:] == 0).all())
+        for n in np.flatnonzero(done):
+            held[n] = held[n][:0]
+    assert refused
+
+
+def test_prefill_reads_back_what_decode_attends_to():
+    """Rows gathered from the cache are the keys of the attention: the absorbed form in float64 on the gathered rows
+    gives the call's outputs."""
+    R, Dr, H, page = 256, 64, 12, 16
+    q, cache, table, lens, cu = _paged(33, [130, 47, 0], page, H, R, Dr, q_lens=[30, 47, 0])
+    rows, _ = in_fp4(cache, R)
+    dev = _cuda(q, rows, _i32(table), _i32(lens), _i32(cu))
+    o, lse = mla.paged_attn_fp4(*dev[:4], R, 0.07, cu_seqlens=dev[4])
+    ends = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    keys = mla.cache_gather_fp4(dev[1], dev[2], _i32(ends).cuda(), int(ends[-1]), R).cpu().double().numpy()
+    for n in range(2):
+        k = keys[ends[n]:ends[n + 1]]
+        x = slice(int(cu[n]), int(cu[n + 1]))
+        for h in range(H):
+            want = orc.attend(q[x, h].double().numpy(), k, k[:, :R], len(k) - (x.stop - x.start), 0.07)
+            _within("read back", o[x, h], want[0], want[2])
+
+
+def test_two_fp4_calls_at_once_on_two_streams():
+    args = []
+    for i in range(2):
+        q, cache, table, lens, cu = _paged(27 + i, [3000, 500], 64, 12, 512, 64)
+        args.append(_cuda(q, in_fp4(cache, 512)[0], _i32(table), _i32(lens)))
+    want = [mla.paged_attn_fp4(*a, 512, 0.07) for a in args]
+    state = [pages(40 + i, 1200, 6, 16) for i in range(2)]
+    plans = [_cuda(_i32(np.full(1200, 3)), *map(_i32, s)) for s in state]
+    want_p = [mla.cache_plan(*p, 16, 3700) for p in plans]
+    torch.cuda.synchronize()
+    streams, got, got_p = [torch.cuda.Stream() for _ in args], [], []
+    for _ in range(3):
+        for s, a, p in zip(streams, args, plans):
+            with torch.cuda.stream(s):
+                got.append(mla.paged_attn_fp4(*a, 512, 0.07))
+                got_p.append(mla.cache_plan(*p, 16, 3700))
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+    for i, p in enumerate(got_p):
+        for n in p:
+            assert torch.equal(p[n], want_p[i % 2][n]), n
