@@ -29,10 +29,7 @@
 // goes through all the sequences' lengths to find its run: 65,536 sequences of
 // 16 rows, H1 R128, take 0.9 ms, 4,096 of them 61 us.
 
-#include <limits.h>
-#include <math.h>
-
-#include "mla_tile.h"
+#include "mla_split.h"
 
 namespace mla {
 namespace {
@@ -44,7 +41,7 @@ constexpr int kPlaces = 16;  // tiles whose rows' places are looked up at a time
 struct PagedPlan {
   int wq;             // wavefronts of 32 rows in a block
   int groups;         // workgroups
-  size_t ml, o, total;  // workspace: unit prefix of the sequences at 0, (maximum, sum) rows, partial sums
+  SplitSpace space;
 };
 
 // Block height by the rows a sequence has, the smallest that holds them or 128:
@@ -63,37 +60,8 @@ PagedPlan paged_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
   const long long most = R == 128 ? 512 : 256, units = blocks * (tiles > 0 ? tiles : 1);
   p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
-  const size_t slots = 2 * (size_t)p.groups * 32 * p.wq;
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  p.ml = up(((size_t)N + 1) * sizeof(long long));
-  p.o = p.ml + up(slots * 2 * sizeof(float));
-  p.total = p.o + slots * R * sizeof(float);
+  p.space = split_space(N, p.groups, 32 * p.wq, R);
   return p;
-}
-
-struct PagedWork {
-  PagedArgs a;
-  long long* prefix;  // [N + 1]: units before sequence n
-  float* ml;          // [2 * groups][block rows][2]
-  float* po;          // [2 * groups][block rows][R]
-};
-
-// A sequence's share: its rows of q, its cache length and its units.
-struct Sequence {
-  int first, Lq, L, blocks, tiles;
-  __device__ __forceinline__ long long units() const { return (long long)blocks * tiles; }
-};
-template <int ROWS>
-__device__ __forceinline__ Sequence sequence(const PagedArgs& a, int n) {
-  Sequence s;
-  int last = n + 1;
-  s.first = n;
-  if (a.cu) document(a.cu, a.Tq, n, s.first, last);
-  s.Lq = last - s.first;
-  s.L = min(max(a.lens[n], 0), a.max_pages * a.page_size);
-  s.blocks = (s.Lq * a.H + ROWS - 1) / ROWS;
-  s.tiles = max((s.L + kTile - 1) / kTile, 1);
-  return s;
 }
 
 template <int R, int DR, int WQ>
@@ -111,8 +79,6 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   constexpr int D = C::D;
   __shared__ __align__(1024) bf16 lat[2][kTile * R];
   __shared__ __align__(1024) bf16 rot[2][DR ? kTile * DR : 8];
-  __shared__ long long scan[C::kWaves + 1];
-  __shared__ long long found[2];
   __shared__ int places[kPlaces * kTile];
   __shared__ __align__(16) u32x4 handed[C::WD > 1 ? WQ : 1][2][2][64];  // weights of the tile's halves, as B operands
   __shared__ float rise[2][C::kRows], sums[2][C::kRows];
@@ -120,56 +86,12 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wd = wave / WQ;
 
-  // ---- this workgroup's run of units ----
-  // Inclusive sum over the workgroup of one value a thread; the total in scan[kWaves].
-  auto block_scan = [&](long long x) {
-    for (int m = 1; m < 64; m <<= 1) {
-      const long long y = __shfl_up(x, m);
-      if (lane >= m) x += y;
-    }
-    __syncthreads();
-    if (lane == 63) scan[wave] = x;
-    __syncthreads();
-    long long before = 0, all = 0;
-    for (int i = 0; i < C::kWaves; ++i) {
-      if (i < wave) before += scan[i];
-      all += scan[i];
-    }
-    __syncthreads();
-    if (tid == 0) scan[C::kWaves] = all;
-    __syncthreads();
-    return x + before;
-  };
-  long long total = 0, mine_units = 0, incl = 0;
-  for (int n0 = 0; n0 < a.N; n0 += C::kThreads) {
-    const int n = n0 + tid;
-    mine_units = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
-    incl = block_scan(mine_units) + total;
-    if (blockIdx.x == 0 && n < a.N) w.prefix[n] = incl - mine_units;
-    total += scan[C::kWaves];
-  }
-  if (blockIdx.x == 0 && tid == 0) w.prefix[a.N] = total;
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
-  const long long begin = share * blockIdx.x, end = min(begin + share, total);
-  if (begin >= end) return;
-  long long before = 0;
-  for (int n0 = 0; n0 < a.N; n0 += C::kThreads) {
-    if (a.N > C::kThreads) {
-      const int n = n0 + tid;
-      mine_units = n < a.N ? sequence<C::kRows>(a, n).units() : 0;
-      incl = block_scan(mine_units) + before;
-      before += scan[C::kWaves];
-    }
-    if (incl - mine_units <= begin && begin < incl) {
-      found[0] = n0 + tid;
-      found[1] = incl - mine_units;
-    }
-    if (begin < before) break;
-  }
-  __syncthreads();
-  int n = (int)found[0];
-  long long base = found[1];  // units before sequence n
-  Sequence sq = sequence<C::kRows>(a, n);
+  Run run;
+  Sequence sq;
+  if (!find_run<C::kRows, kTile>(w, run, sq)) return;
+  const long long begin = run.begin, end = run.end;
+  int n = run.n;
+  long long base = run.base;  // units before sequence n
   const float c = a.scale * kda::kLog2e;
   const unsigned lds_lat = lds_address(&lat[0][0]), lds_rot = lds_address(&rot[0][0]);
   const LaneAt<R> at_lat(lane);
@@ -180,7 +102,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   for (long long u = begin; u < end;) {
     while (u >= base + sq.units()) {
       base += sq.units();
-      sq = sequence<C::kRows>(a, ++n);
+      sq = sequence<C::kRows, kTile>(a, ++n);
     }
     const int block = (int)((u - base) / sq.tiles), t0 = (int)((u - base) % sq.tiles);
     const int t1 = (int)min((long long)sq.tiles, t0 + (end - u));
@@ -409,102 +331,18 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   }
 }
 
-// Joins the parts of split blocks: a wavefront a row for few parts, or for many
-// a workgroup for 64 channels of a row, 16 parts at a time.
-template <int R, int ROWS, bool MANY>
-__global__ __launch_bounds__(256) void combine_kernel(PagedWork w, int groups) {
-  constexpr int kSlice = MANY ? 64 : R, kAcross = kSlice / 4;      // threads over the channels
-  constexpr int kLanes = MANY ? 256 : 64, kWays = MANY ? kLanes / kAcross : 1;  // threads of a row, parts at a time
-  constexpr int kQuads = MANY ? 1 : R / 256 > 0 ? R / 256 : 1;      // 4-channel pieces a thread (few parts)
-  const PagedArgs& a = w.a;
-  const int tid = threadIdx.x;
-  const long long row = MANY ? blockIdx.x / (R / 64) : (long long)blockIdx.x * 4 + (tid >> 6);
-  if (row >= (long long)a.Tq * a.H) return;
-  int n = (int)(row / a.H);
-  if (a.cu) {
-    int lo = 0, hi = a.N;
-    const int token = n;
-    while (hi - lo > 1) {  // the last sequence that starts at or before the token
-      const int step = (hi - lo + 63) / 64, i = lo + (tid & 63) * step;
-      const int count = __popcll(__ballot(i < hi && min(max(a.cu[i], 0), a.Tq) <= token));
-      lo += max(count - 1, 0) * step;
-      hi = min(lo + step, hi);
-    }
-    n = lo;
-  }
-  const Sequence s = sequence<ROWS>(a, n);
-  const long long in = row - (long long)s.first * a.H;
-  if (in < 0 || in >= (long long)s.Lq * a.H) return;
-  const long long share = (w.prefix[a.N] + groups - 1) / groups;
-  const long long u0 = w.prefix[n] + in / ROWS * s.tiles, u1 = u0 + s.tiles - 1;
-  const int g0 = (int)(u0 / share), g1 = (int)(u1 / share);
-  if (g0 == g1) return;  // in one piece: written already
-  // part g's slot: its run's first segment, unless the block starts inside the run
-  auto place = [&](int g) { return (long long)(2 * g + (g == g0 && u0 != g0 * share ? 1 : 0)) * ROWS + in % ROWS; };
-  float m = -FLT_MAX;
-  for (int g = g0 + (tid & 63); g <= g1; g += 64) m = fmaxf(m, w.ml[2 * place(g)]);
-#pragma unroll
-  for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
-  float l = 0.f;
-  f32x4 o[kQuads] = {};
-  const int way = MANY ? tid / kAcross : 0;
-  const int ch = MANY ? (blockIdx.x % (R / 64)) * 64 + (tid % kAcross) * 4 : (tid & 63) * 4;
-  const bool in_row = MANY || ch < R;
-#pragma unroll 8
-  for (int g = g0 + way; g <= g1; g += kWays) {
-    const long long at = place(g);
-    const float f = kda::fast_exp2(w.ml[2 * at] - m);
-    l += w.ml[2 * at + 1] * f;
-    if (in_row) {
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q) o[q] += *(const f32x4*)(w.po + at * R + ch + 256 * q) * f;
-    }
-  }
-  if constexpr (MANY) {
-    __shared__ f32x4 part[kWays][kAcross];
-    __shared__ float lpart[kWays];
-    part[way][tid % kAcross] = o[0];
-    if (tid % kAcross == 0) lpart[way] = l;
-    __syncthreads();
-    if (way != 0) return;
-    for (int i = 1; i < kWays; ++i) {
-      o[0] += part[i][tid];
-      l += lpart[i];
-    }
-  }
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  if (in_row) {
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q)
-      *(u32x2*)(a.o + row * R + ch + 256 * q) =
-          u32x2{kda::pk_bf16(o[q][0] * r, o[q][1] * r), kda::pk_bf16(o[q][2] * r, o[q][3] * r)};
-  }
-  if (a.lse && ch == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kda::kLog2e);
-}
-
 template <int R, int DR, int WQ>
 hipError_t launch(const PagedWork& w, const PagedPlan& p, hipStream_t stream) {
   using C = Paged<R, DR, WQ>;
   paged_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w);
-  if (p.groups > 1) {
-    const long long rows = (long long)w.a.Tq * w.a.H;
-    // Parts a block can have: with more than 8 a row takes several workgroups (8 rows of 15 parts: 4.2 us, with a
-    // wavefront a row 9.7 us; 6,144 rows of about 5 parts: 38 us, with a wavefront a row 13.5 us).
-    if (p.groups > 8 * (rows / C::kRows + 1))
-      combine_kernel<R, C::kRows, true><<<dim3((unsigned)(rows * (R / 64))), dim3(256), 0, stream>>>(w, p.groups);
-    else
-      combine_kernel<R, C::kRows, false><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(w, p.groups);
-  }
+  launch_combine<R, C::kRows, kTile>(w, p.groups, stream);
   return hipGetLastError();
 }
 
 template <int R, int DR>
 hipError_t launch(const PagedArgs& a, hipStream_t stream) {
   const PagedPlan p = paged_plan(a.N, a.Tq, a.H, R, DR, (long long)a.max_pages * a.page_size);
-  char* ws = static_cast<char*>(a.ws);
-  PagedWork w{a, reinterpret_cast<long long*>(ws), reinterpret_cast<float*>(ws + p.ml),
-              reinterpret_cast<float*>(ws + p.o)};
-  if (a.num_pages == 0) w.a.max_pages = 0;  // no cache rows at all: every length is 0
+  const PagedWork w = split_work(a, p.space);
   switch (p.wq) {
     case 1: return launch<R, DR, 1>(w, p, stream);
     case 2: return launch<R, DR, 2>(w, p, stream);
@@ -515,7 +353,7 @@ hipError_t launch(const PagedArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t paged_workspace(int N, int Tq, int H, int R, int Dr, long long max_len) {
-  return N == 0 || Tq == 0 ? 0 : paged_plan(N, Tq, H, R, Dr, max_len).total;
+  return N == 0 || Tq == 0 ? 0 : paged_plan(N, Tq, H, R, Dr, max_len).space.total;
 }
 
 hipError_t launch_paged(int R, int Dr, const PagedArgs& a, hipStream_t stream) {
