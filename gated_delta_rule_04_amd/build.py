@@ -52,7 +52,7 @@ SOURCE_FLAGS = {
     "mla_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     # The same for the 4-bit paged attention (512 channels, 96 rows: 209 spills
     # without); with the target's own register-pressure trackers it takes 481 registers.
-    "mla_paged_fp4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1", "-mllvm", "-amdgpu-use-amdgpu-trackers=1"],
+    "mla_paged_fp4.hip": [],
 }
 
 
