@@ -36,6 +36,11 @@ constexpr int kPlaces = 16;  // tiles whose rows' places are looked up at a time
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+// Said to be global: an access that may be LDS too is counted with those of the LDS, and waited for with them.
+typedef __attribute__((address_space(1))) u32x4 global_u32x4;
+typedef __attribute__((address_space(1))) u32x2 global_u32x2;
+typedef __attribute__((address_space(1))) unsigned short global_u16;
+typedef __attribute__((address_space(1))) unsigned char global_u8;
 
 struct Fp4Plan {
   int rb;      // 32-row blocks
@@ -204,21 +209,21 @@ __global__ __launch_bounds__(256, RB == 1 ? 2 : 1) void paged_fp4_kernel(PagedWo
       };
       // Tile t's part from its place on; which of its rows are there.
       auto fetch = [&](Raw<KS>& x, int from) {
-        const unsigned char* row = opaque(a.cache4 + (long long)max(from, 0) * C::kRow);
+        const auto row = (const global_u8*)opaque((unsigned long long)a.cache4 + (long long)max(from, 0) * C::kRow);
         const int h = opaque(lane) >> 5, code_at = wave * (CW / 2) + h * (CW / 4), pe_at = R / 2 + wave * 32 + h * 16;
         const int scale_at = R / 2 + 2 * DR + (R == 512 ? 4 * wave + 2 * h : R == 256 ? 2 * wave + h : wave);
         if constexpr (KS == 8) {
-          *(u32x4*)x.code = *(const u32x4*)(row + code_at);
-          *(u32x4*)(x.code + 4) = *(const u32x4*)(row + code_at + 16);
-          x.scale = *(const unsigned short*)(row + scale_at);
+          *(u32x4*)x.code = *(const global_u32x4*)(row + code_at);
+          *(u32x4*)(x.code + 4) = *(const global_u32x4*)(row + code_at + 16);
+          x.scale = *(const global_u16*)(row + scale_at);
         } else if constexpr (KS == 4) {
-          *(u32x4*)x.code = *(const u32x4*)(row + code_at);
+          *(u32x4*)x.code = *(const global_u32x4*)(row + code_at);
           x.scale = row[scale_at];
         } else {
-          *(u32x2*)x.code = *(const u32x2*)(row + code_at);
+          *(u32x2*)x.code = *(const global_u32x2*)(row + code_at);
           x.scale = row[scale_at];
         }
-        if constexpr (DR > 0) x.pe = *(const u32x4*)(row + pe_at);
+        if constexpr (DR > 0) x.pe = *(const global_u32x4*)(row + pe_at);
         return (unsigned)__ballot(from >= 0);
       };
       f32x4 own[RB];  // this wavefront's part of its share of the scores
