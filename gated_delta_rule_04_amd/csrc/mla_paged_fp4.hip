@@ -1,28 +1,30 @@
 // Absorbed latent attention over the paged 4-bit cache.
 //
-// The work is cut as in mla_split.h, in blocks of 32 RB rows and tiles of 32 cache
-// rows.  A workgroup has 4 wavefronts, and they split the channels: each holds a
-// quarter of the block's queries (R / 4 latent channels and a quarter of the rotary
-// ones) and of O^T, for all rows of the block.  So each needs only its own quarter
-// of a tile, for the scores and for the sums: it loads it from the pages straight
-// into the layout of the products' A operand (a lane holds a row's 8 channels of a
-// step in one register of codes), converts it there (v_cvt_scalef32_pk_bf16_fp4:
-// exact), and puts it as bf16 into LDS of its own for the transposing reads of
-// O^T += C^T P^T; no part of a tile passes between wavefronts.  What does is the
-// scores: S^T = C Q^T over a quarter of the channels is a partial sum, of which
-// each wavefront finishes the 8 rows of the tile that are its share, so that no
-// exponential is taken twice, and hands the weights to all.
+// The work is cut as in mla_split.h, in blocks of 32 WQ rows and tiles of 32 cache
+// rows.  A workgroup has 4 wavefronts: WQ of them take 32 rows of the block each,
+// and the WT = 4 / WQ groups of such take the tiles in turn.  A wavefront holds its
+// rows' queries (vector registers) and their O^T for all channels (accumulators;
+// at R = 512 all of them).
 //
-// In the pass over the tiles, an interval between two barriers forms the weights
-// of tile i + 1, the sums of tile i and the partial scores of tile i + 2, which do
-// not wait for each other.
+// A tile's codes go from the pages into registers, in the layout of the products'
+// A operand: a lane holds half a row, 8 channels of a step in one register, and
+// converts them as they are needed (v_cvt_scalef32_pk_bf16_fp4: exact).  S^T = C
+// Q^T, the softmax a row a lane, and the weights are the B operand of O^T += C^T P^T
+// as they are.  Its A operand is read by transposing reads from LDS, where the
+// converted tile is put, by each of the WQ wavefronts in part; with WQ = 1 nothing
+// passes between wavefronts and there is no barrier.  The products of tile i + 1's
+// scores and of tile i's sums alternate, and each register of codes is loaded
+// again, for the tile after, as soon as it has been converted.
 //
 // The exponentials of a row have one reference through a run of tiles, the largest
 // score of the first: bf16 weights and float32 sums lose nothing by a reference
-// that is below the row's largest score by 2^30.  Where a score passes it by more,
-// or a sum is not finite, the run is done again with the largest score of all its
-// tiles, found first; so a run takes three passes at most, and the loop has no
-// rescaling of the sums, which would cost it their place in the accumulators.
+// that is below the row's largest score by 2^30, while values stay below 2^68 (the
+// sums of 2^27 of them below 2^125).  Where a score passes it by more, or a scale
+// is 2^65 or more, the run is done again with the largest score of all its tiles,
+// found first; so a run takes three passes at most, and the loop has no rescaling
+// of the sums, which would cost them their place in the accumulators.
+
+#include <type_traits>
 
 #include "mla_fp4.h"
 #include "mla_split.h"
@@ -30,20 +32,18 @@
 namespace mla {
 namespace {
 
-constexpr int kTile = 32;    // cache rows of a tile
-constexpr int kPlaces = 16;  // tiles whose rows' places are looked up at a time
+constexpr int kTile = 32;  // cache rows of a tile
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 // Said to be global: an access that may be LDS too is counted with those of the LDS, and waited for with them.
-typedef __attribute__((address_space(1))) u32x4 global_u32x4;
-typedef __attribute__((address_space(1))) u32x2 global_u32x2;
-typedef __attribute__((address_space(1))) unsigned short global_u16;
-typedef __attribute__((address_space(1))) unsigned char global_u8;
+typedef __attribute__((address_space(1))) const u32x4 global_u32x4;
+typedef __attribute__((address_space(1))) const u32x2 global_u32x2;
+typedef __attribute__((address_space(1))) const unsigned global_u32;
+typedef __attribute__((address_space(1))) const char global_char;
 
 struct Fp4Plan {
-  int rb;      // 32-row blocks
+  int wq;      // wavefronts of 32 rows in a block
   int groups;  // workgroups
   SplitSpace space;
 };
@@ -51,22 +51,11 @@ struct Fp4Plan {
 Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   Fp4Plan p;
   const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
-  const int most_rb = R == 512 ? 3 : 4;
-  p.rb = 1;
-  long long best = -1;
-  for (int rb = 1; rb <= most_rb; ++rb) {
-    const long long cost = (per + 32 * rb - 1) / (32 * rb) * (rb + 1);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.rb = rb;
-    }
-  }
-  const long long blocks = rows / (32 * p.rb) + N, tiles = (max_len + kTile - 1) / kTile;
-  const int lds = 28 * 1024 * p.rb + 64 * R + 4096;  // of a workgroup, and what is static
-  const long long most = 256 * (160 * 1024 / lds < 1 ? 1 : 160 * 1024 / lds > 4 ? 4 : 160 * 1024 / lds);
-  const long long units = blocks * (tiles > 0 ? tiles : 1);
+  p.wq = per <= 32 ? 1 : per <= 64 ? 2 : 4;
+  const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
+  const long long most = 256, units = blocks * (tiles > 0 ? tiles : 1);
   p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
-  p.space = split_space(N, p.groups, 32 * p.rb, R);
+  p.space = split_space(N, p.groups, 32 * p.wq, R);
   return p;
 }
 
@@ -76,6 +65,11 @@ template <typename T>
 __device__ __forceinline__ T opaque(T x) {
   asm("" : "+v"(x));
   return x;
+}
+
+// The lane, found again where it is used.
+__device__ __forceinline__ int lane_id() {
+  return opaque((int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)));
 }
 
 // Division by a number that is the same for all, for dividends below 2^31: with
@@ -92,35 +86,38 @@ struct Divide {
   __device__ __forceinline__ unsigned of(unsigned n) const { return (unsigned)(((unsigned long long)n * m) >> shift); }
 };
 
-template <int R, int DR, int RB>
+template <int R, int DR, int WQ>
 struct Fp4 {
-  static constexpr int kThreads = 256, kRows = 32 * RB, kRow = fp4_row_bytes(R, DR);
-  static constexpr int CW = R / 4, KS = CW / 16, DT = CW / 32;  // a wavefront's channels, steps of its scores, tiles of its sums
-  // In LDS, 1024 bytes (16 a lane) a piece: partial scores [2][of wavefront][from 3][RB], weights as B operands
-  // [2][RB][2]; then each wavefront's values of two tiles.
-  static constexpr int kPart = 0, kWeight = kPart + 24 * RB * 1024, kVal = kWeight + 4 * RB * 1024;
-  static constexpr int kValTile = kTile * CW * 2, kLds = kVal + 8 * kValTile;
-  static constexpr int kAhead = RB < 3 ? 4 : 2;  // tiles in registers, on their way or there
+  static constexpr int kThreads = 256, kRows = 32 * WQ, kRow = fp4_row_bytes(R, DR), WT = 4 / WQ;
+  static constexpr int KS = R / 16, PS = DR / 16;  // steps of 16 channels: of the latent, of the rotary key
+  static constexpr int kOut = R / 32;              // 32-channel tiles of O^T
+  // A lane's part of a row is loaded in pieces of E steps (E registers of codes), those of the two halves of the lanes
+  // side by side: step s = E p + i is of channels 16 E p + 8 E half + 8 i.
+  static constexpr int E = R == 128 ? 2 : 4, kPieces = KS / E, kScales = R / 128;
+  static constexpr int kTurn = kPieces / WQ;  // the wavefronts of a tile begin so many pieces apart, and put the first
+                                              // kTurn of their pieces into LDS for all
+  // At R = 512 there are no registers for all of the queries: the rotary part and those of some steps are in LDS.
+  static constexpr bool far(int s) { return R == 512 && (s >= KS || s % 4 == 3 || (WQ != 2 && s % 8 == 1)); }
+  static constexpr int far_at(int s) {  // 1024 bytes a step
+    int n = 0;
+    for (int i = 0; i < s; ++i) n += far(i);
+    return 1024 * n;
+  }
+  static constexpr int kVal = kTile * R * 2, kBuffers = WQ == 1 ? 1 : 2;  // bytes of a tile's values, tiles of a group
+  static constexpr int kQuery = WT * kBuffers * kVal, kQueries = far_at(KS + PS);
+  static constexpr int kLds = kQuery + WQ * kQueries;
 };
 
-// A lane's part of a tile: its row's codes, scales and rotary key.
-template <int KS>
-struct Raw {
-  unsigned code[KS];
-  unsigned scale;
-  u32x4 pe;
-};
-
-template <int R, int DR, int RB>
-__global__ __launch_bounds__(256, RB == 1 ? 2 : 1) void paged_fp4_kernel(PagedWork w, Divide by_page) {
-  using C = Fp4<R, DR, RB>;
-  constexpr int D = R + DR, CW = C::CW, KS = C::KS, DT = C::DT, QS = KS + (DR ? 1 : 0);
+template <int R, int DR, int WQ>
+__global__ __launch_bounds__(256, 1) void paged_fp4_kernel(PagedWork w, Divide by_page) {
+  using C = Fp4<R, DR, WQ>;
+  constexpr int D = R + DR, KS = C::KS, PS = C::PS, kOut = C::kOut, WT = C::WT, kRow = C::kRow;
   __shared__ __align__(1024) char lds[C::kLds];
-  __shared__ float top[4][C::kRows];
-  __shared__ int places[2][kPlaces * kTile];  // cache rows, -1 where there is none: of two groups of tiles
+  __shared__ float top[4][32], sums[4][32];
+  __shared__ int flags[4];
   const PagedArgs& a = w.a;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wt = wave / WQ;
   Run run;
   Sequence sq;
   if (!find_run<C::kRows, kTile>(w, run, sq)) return;
@@ -130,13 +127,12 @@ __global__ __launch_bounds__(256, RB == 1 ? 2 : 1) void paged_fp4_kernel(PagedWo
   int n = uniform((unsigned)run.n);
   sq = sequence<C::kRows, kTile>(a, n);
   const float c = a.scale * kda::kLog2e;
-  // The row of a tile that a lane loads is (lane + 8 wave) % 32, so that a wavefront's own share of the scores is always
-  // the first group of 4 registers.
-  const LaneAt<CW> at(lane);
-  // LDS addresses: of the lane's 16 bytes of a piece
-  const unsigned lds0 = lds_address(&lds[0]), mine16 = lds0 + 16 * lane;
-  // of the values: a piece of 8 channels of the row that the lane loads, piece s at put_at ^ 16 s
-  const unsigned val_at = lds0 + C::kVal + wave * (2 * C::kValTile);
+  const LaneAt<R> at(lane);
+  const unsigned lds0 = lds_address(&lds[0]), val = lds0 + wt * (C::kBuffers * C::kVal);
+  const unsigned query = lds0 + C::kQuery + wq * C::kQueries + lane * 16;  // the same for wavefronts of the same rows
+  // The lane's row of a tile in LDS, its part of piece p (16 E bytes of 32 E) at (put ^ 32 E p % 256) + 256 (32 E p / 256)
+  constexpr int E = C::E, kPieces = C::kPieces, kTurn = C::kTurn;
+  const unsigned put = l32 * (R * 2) + ((E * half) ^ swizzle<R>(l32)) * 16;
 
   for (long long u = begin; u < end;) {
     while (u >= base + sq.units()) {
@@ -152,385 +148,356 @@ __global__ __launch_bounds__(256, RB == 1 ? 2 : 1) void paged_fp4_kernel(PagedWo
     // the last cache row that a row of the block sees
     const int seen = sq.L - sq.Lq + (min(rows, m0 + C::kRows) - 1) / a.H;
     const int stop = min(t1, seen < 0 ? 0 : seen / kTile + 1), count = stop - t0;
+    // this wavefront's tiles: t0 + wt + WT i for i < turns; with barriers in the loop, all wavefronts go round as often
+    const int turns = count <= 0 ? 0 : WQ == 1 ? (count - wt + WT - 1) / WT : (count + WT - 1) / WT;
     const int* table = a.table + (long long)n * a.max_pages;
-    int lim[RB];  // the last cache row that the lane's row sees
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const int mi = m0 + 32 * r + l32;
-      lim[r] = mi < rows ? sq.L - sq.Lq + mi / a.H : INT_MAX;
-    }
+    const int last = min(stop * kTile, sq.L);  // behind the last row of the run
+    const int mi = m0 + 32 * wq + l32;
+    const bool on = mi < rows;
+    const int lim = on ? sq.L - sq.Lq + mi / a.H : INT_MAX;  // the last cache row that the lane's row sees
+    const bool idle = m0 + 32 * wq >= rows;  // no rows of its own: only its part of the values
 
-    f32x16 acc[RB][DT];
-    float m[RB], l[RB];
+    f32x16 acc[kOut];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      m[r] = -FLT_MAX, l[r] = 0.f;
+    for (int d = 0; d < kOut; ++d) acc[d] = f32x16{};
+    float m = -FLT_MAX, l = 0.f;
+    if (WQ > 1) lds_barrier();  // the run before is done with the LDS
+    if (turns > 0) {
+      bf16x8 qf[KS + PS];
+      auto load_query = [&] {  // a row that is not one reads the last again, and is not written
+        const bf16* q = a.q + ((long long)sq.first * a.H + min(m0 + 32 * wq + (lane_id() & 31), rows - 1)) * D;
+        const int h = lane_id() >> 5;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) acc[r][d] = f32x16{};
-    }
-    if (count > 0) {
-      bf16x8 qf[RB][QS];
-#pragma unroll
-      for (int r = 0; r < RB; ++r) {  // a row that is not one reads the last again, and is not written
-        const bf16* q = a.q + ((long long)sq.first * a.H + min(m0 + 32 * r + l32, rows - 1)) * D;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) qf[r][s] = *(const bf16x8*)(q + wave * CW + half * (CW / 2) + 8 * s);
-        if constexpr (DR > 0) {
-          qf[r][KS] = *(const bf16x8*)(q + R + wave * 16 + half * 8);
-          if constexpr (RB == 3 && KS == 8) asm("" : "+a"(qf[r][KS]));
+        for (int s = 0; s < KS + PS; ++s) {
+          const int p = (s / E + wq * kTurn) % kPieces;
+          qf[s] = *(const bf16x8*)(s < KS ? q + 16 * E * p + 8 * E * h + 8 * (s % E) : q + R + 16 * (s - KS) + 8 * h);
+          if (C::far(s)) *(lds_u32x4*)(query + C::far_at(s)) = __builtin_bit_cast(u32x4, qf[s]);
+          if (s % 8 == 7) __builtin_amdgcn_sched_barrier(0);  // else more are on their way than there are registers
         }
-      }
-
-      constexpr int kAhead = C::kAhead;
-      Raw<KS> raw[kAhead];  // tile t in raw[t % kAhead]
-      unsigned bits[kAhead + 1];  // rows of tiles i + 1 .. that are there, bit of lane l32
-      // The places of the rows of group g of tiles: looked up, then put into LDS.  (Compared without a sign: a group may
-      // begin behind all the rows that 31 bits count.)
-      const int last = min((t0 + count) * kTile, sq.L);
-      int page[2];
-      auto look_up = [&](int g) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = (t0 + g * kPlaces) * kTile + tid + 256 * e;
-          page[e] = -1;
-          if ((unsigned)j < (unsigned)last) page[e] = table[by_page.of(j)];
-        }
-      };
-      auto put_places = [&](int g) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = (t0 + g * kPlaces) * kTile + tid + 256 * e;
-          const int off = j - (int)by_page.of(j) * a.page_size;
-          places[g & 1][tid + 256 * e] = (unsigned)page[e] < (unsigned)a.num_pages ? page[e] * a.page_size + off : -1;
-        }
-      };
-      auto place = [&](int t) {
-        return (&places[0][0])[(t & (2 * kPlaces - 1)) * kTile + ((opaque(lane) + 8 * wave) & 31)];
-      };
-      // Tile t's part from its place on; which of its rows are there.
-      auto fetch = [&](Raw<KS>& x, int from) {
-        const auto row = (const global_u8*)opaque((unsigned long long)a.cache4 + (long long)max(from, 0) * C::kRow);
-        const int h = opaque(lane) >> 5, code_at = wave * (CW / 2) + h * (CW / 4), pe_at = R / 2 + wave * 32 + h * 16;
-        const int scale_at = R / 2 + 2 * DR + (R == 512 ? 4 * wave + 2 * h : R == 256 ? 2 * wave + h : wave);
-        if constexpr (KS == 8) {
-          *(u32x4*)x.code = *(const global_u32x4*)(row + code_at);
-          *(u32x4*)(x.code + 4) = *(const global_u32x4*)(row + code_at + 16);
-          x.scale = *(const global_u16*)(row + scale_at);
-        } else if constexpr (KS == 4) {
-          *(u32x4*)x.code = *(const global_u32x4*)(row + code_at);
-          x.scale = row[scale_at];
-        } else {
-          *(u32x2*)x.code = *(const global_u32x2*)(row + code_at);
-          x.scale = row[scale_at];
-        }
-        if constexpr (DR > 0) x.pe = *(const global_u32x4*)(row + pe_at);
-        return (unsigned)__ballot(from >= 0);
-      };
-      f32x4 own[RB];  // this wavefront's part of its share of the scores
-      f32x16 S[RB];   // partial scores of a tile; register i: the lane's row, tile row acc_row(i) + 8 wave
-      // 8 channels of step s, as an A operand
-      auto channels = [&](const Raw<KS>& x, int s) {
-        if (s >= KS) return x.pe;
-        const unsigned byte = KS == 8 && s >= 4 ? x.scale >> 8 : x.scale & 255;
-        return fp4_values(x.code[s], __builtin_bit_cast(float, byte << 23));
-      };
-      // The partial scores of a tile, and its values into val_at[b].  The next step's operand is converted beside this
-      // step's products; `last` is done beside the last ones.
-      auto scores = [&](const Raw<KS>& x, int b, auto last) {
-        const int me = opaque(lane), row = (me + 8 * wave) & 31;
-        const unsigned to = opaque(val_at + b * C::kValTile + row * (CW * 2) + (((me >> 5) * KS) ^ swizzle<CW>(row)) * 16);
-        u32x4 k = channels(x, 0);
-#pragma unroll
-        for (int s = 0; s < QS; ++s) {
-          u32x4 next = k;
-          if (s + 1 < QS) next = channels(x, s + 1);
-          if (s < KS) *(lds_u32x4*)(to ^ (16 * s)) = k;
-#pragma unroll
-          for (int r = 0; r < RB; ++r)
-            S[r] = mma(__builtin_bit_cast(bf16x8, k), qf[r][s], s == 0 ? f32x16{} : S[r]);
-          k = next;
-          if (s == QS - 1) last();
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      };
-      auto hand = [&](int r, int b) {
-        own[r] = f32x4{S[r][0], S[r][1], S[r][2], S[r][3]};
-#pragma unroll
-        for (int g = 1; g < 4; ++g)
-          *(lds_f32x4*)(opaque(mine16 + C::kPart + ((wave + g) & 3) * (3 * RB * 1024)) +
-                        ((4 * b * 3 + 3 - g) * RB + r) * 1024) =
-              f32x4{S[r][4 * g], S[r][4 * g + 1], S[r][4 * g + 2], S[r][4 * g + 3]};
-      };
-      auto part = [&](int b, int g, int r) {
-        return *(const lds_f32x4*)(opaque(mine16 + C::kPart + wave * (3 * RB * 1024)) + ((4 * b * 3 + g) * RB + r) * 1024);
-      };
-      auto weight = [&](int b, int r, int s) {
-        return __builtin_bit_cast(bf16x8, *(const lds_u32x4*)(opaque(mine16) + C::kWeight + ((b * RB + r) * 2 + s) * 1024));
-      };
-      auto highest = [&](const f32x4& x) { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c; };
-      bool passed = false;  // a score is above its reference by more than 2^30
-      auto rows_of = [&](int t, unsigned in, int* j) {  // of this lane's share of tile t; absent ones behind all
-#pragma unroll
-        for (int k = 0; k < 4; ++k) j[k] = (t0 + t) * kTile + 8 * wave + 4 * (opaque(lane) >> 5) + k;
-        if (in != ~0u) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) j[k] = (in >> (4 * (opaque(lane) >> 5) + k)) & 1 ? j[k] : INT_MAX;
-        }
-      };
-      auto mask = [&](int r, f32x4& x, const int* j) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = j[k] > lim[r] ? -INFINITY : x[k];
-      };
-      auto softmax = [&](int r, const f32x4& x, int b) {  // weights of the rows r of the share x
-        float p[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = kda::fast_exp2(__builtin_fmaf(x[k], c, -m[r]));
-        l[r] += (p[0] + p[1]) + (p[2] + p[3]);
-        *(lds_u32x2*)(opaque(mine16 + C::kWeight + (wave >> 1) * 1024 + (wave & 1) * 8) + (b * RB + r) * 2048) = u32x2{kda::pk_bf16(p[0], p[1]), kda::pk_bf16(p[2], p[3])};
-        passed |= highest(x) > m[r] + 30.f;
-      };
-      auto clear = [&](Raw<KS>& x, unsigned in) {  // rows that are not there: any finite values
-        if (in != ~0u && !((in >> (opaque(lane) & 31)) & 1)) {
-          x.scale = 0;
-          x.pe = u32x4{};
-        }
-      };
-      // The rows' largest scores of those that the wavefronts found.
-      auto refer = [&](const float* mx) {
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const float x = halves_max(mx[r]);
-          if (half == 0) top[wave][32 * r + l32] = x;
-        }
-        lds_barrier();
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          m[r] = -FLT_MAX;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) m[r] = fmaxf(m[r], top[g][32 * r + l32]);
-        }
-        lds_barrier();
-      };
-      auto share = [&](int t, unsigned in, int b, f32x4* x) {  // the finished and masked share of a tile
-        int j[4];
-        rows_of(t, in, j);
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          x[r] = own[r] + ((part(b, 0, r) + part(b, 1, r)) + part(b, 2, r));
-          mask(r, x[r], j);
-        }
-      };
-
-      // Interval i, b = i % 2, k = i % kAhead: weights of tile i + 1, sums of tile i, partial scores of tile i + 2 (whose values take the
-      // place of tile i's).  Tiles from `count` on have no rows, and add nothing.
-      auto interval = [&](int i, int k) {
-        const int b = k & 1;
-        Raw<KS>& x2 = raw[(k + 2) % kAhead];
-        const int from = place(i + 2 + kAhead);
-        const unsigned tile = opaque(val_at + b * C::kValTile);
-        constexpr int kFirst = DT < 2 ? DT : 2;  // reads of operands ahead of the products
-        bf16x8 p[2][RB], v[2][DT];
-        f32x4 y[RB][3];
-        auto take = [&](int r) {
-#pragma unroll
-          for (int g = 0; g < 3; ++g) y[r][g] = part(b ^ 1, g, r);
-        };
-#pragma unroll
-        for (int r = 0; r < RB; ++r) p[0][r] = weight(b, r, 0);
-#pragma unroll
-        for (int d = 0; d < kFirst; ++d) v[0][d] = tr_frag(tile, at, 0, d);
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-          if (r * DT / RB == 0) take(r);
-        int j[4];
-        rows_of(i + 1, bits[0], j);
-        clear(x2, bits[1]);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          if (d + kFirst < DT) v[0][d + kFirst] = tr_frag(tile, at, 0, d + kFirst);
-          if (DT < 4 || d >= DT - 2) {  // before the next tile's values are put in their place
-            constexpr int kEach = DT < 4 ? 1 : DT / 2;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-              const int f = DT < 4 ? d : (d - (DT - 2)) * kEach + e;
-              v[1][f] = tr_frag(tile, at, 16, f);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < RB; ++r)
-            if (r * DT / RB == d + 1) take(r);
-#pragma unroll
-          for (int r = 0; r < RB; ++r) acc[r][d] = mma(v[0][d], p[0][r], acc[r][d]);
-#pragma unroll
-          for (int r = 0; r < RB; ++r)
-            if (r * DT / RB == d) {
-              f32x4 x = own[r] + ((y[r][0] + y[r][1]) + y[r][2]);
-              mask(r, x, j);
-              softmax(r, x, b ^ 1);
-            }
-          __builtin_amdgcn_sched_barrier(0);
+      };
+      auto far_query = [&](int s) { return __builtin_bit_cast(bf16x8, *(lds_u32x4*)(query + C::far_at(s))); };
+      unsigned code[KS];
+      u32x4 pe[PS > 0 ? PS : 1];
+      unsigned scale[C::kScales], next_scale[C::kScales];
+      // Where the lane's row of a tile lies (its half of each piece, and what follows the codes), whether it is there.
+      int page = -1, off = 0;
+      bool in = false, next_in = false;
+      unsigned long long row = 0, row_end = 0;
+      auto look_up = [&](int i) {  // of tile i: from -1 on all rows are behind the end
+        const int j = (t0 + wt + WT * i) * kTile + l32;
+        page = -1;
+        if ((unsigned)j < (unsigned)last) {
+          const unsigned p = by_page.of(j);
+          off = j - (int)p * a.page_size;
+          page = table[p];
         }
-        scores(x2, b, [&] {
+      };
+      auto find = [&] {  // the tile looked up last is the next
+        next_in = (unsigned)page < (unsigned)a.num_pages;
+        const long long r = next_in ? page * a.page_size + off : 0;
+        row = (unsigned long long)a.cache4 + r * kRow + 4 * E * half;
+        row_end = (unsigned long long)a.cache4 + r * kRow + R / 2 + 16 * half;
+      };
+      auto load_codes = [&](int p) {
+        const auto from = (global_char*)row + 8 * E * ((p + wq * kTurn) % kPieces);
+        if constexpr (E == 4)
+          *(u32x4*)(code + 4 * p) = *(global_u32x4*)from;
+        else
+          *(u32x2*)(code + 2 * p) = *(global_u32x2*)from;
+      };
+      auto load_key = [&](int s) { pe[s] = *(global_u32x4*)((global_char*)row_end + 32 * s); };
+      // The scales in the order of the wavefront's pieces: R / 32 bytes, byte p (E = 2) or 2 p + half (E = 4) of piece p.
+      constexpr int kBytes = E / 2, kRoll = kBytes * kTurn;
+      auto load_scales = [&] {
+        const auto from = (global_char*)row_end - 16 * half + 2 * DR;
 #pragma unroll
-          for (int r = 0; r < RB; ++r) p[1][r] = weight(b, r, 1);
-        });
+        for (int i = 0; i < C::kScales; ++i)
+          next_scale[i] = *(global_u32*)(from + 4 * ((i + wq * kRoll / 4) % C::kScales));
+      };
+      auto turn_scales = [&] {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-#pragma unroll
-          for (int r = 0; r < RB; ++r) acc[r][d] = mma(v[1][d], p[1][r], acc[r][d]);
-          if (d == 0) {
-#pragma unroll
-            for (int e = 0; e < kAhead; ++e) bits[e] = bits[e + 1];
-            bits[kAhead] = fetch(x2, from);
-          }
-#pragma unroll
-          for (int r = 0; r < RB; ++r)
-            if (r * DT / RB == d) hand(r, b);
-          __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < C::kScales; ++i)
+          scale[i] = kRoll % 4 == 0 ? next_scale[i]
+                                    : __builtin_amdgcn_alignbit(next_scale[(i + 1) % C::kScales], next_scale[i],
+                                                                wq * kRoll % 4 * 8);
+      };
+
+      f32x16 S;  // S^T of a tile; register i: the lane's row, tile row acc_row(i)
+      bf16x8 P[2];
+      // 8 channels of step s, as an A operand.  Rows that are not there have a scale of 2^-127: any finite values.
+      auto channels = [&](int s) {
+        const int byte = kBytes * (s / E);  // and half, where a piece has two
+        const unsigned x = scale[byte / 4] >> (8 * (byte % 4) + (E == 4 ? 8 * half : 0));
+        return fp4_values(code[s], __builtin_bit_cast(float, in ? (x & 255) << 23 : 0u));
+      };
+      auto score = [&](u32x4 k, bf16x8 q, bool first) {
+        if constexpr (R == 512) {
+          // In vector registers: the accumulators are full.  (The compiler takes all results of a kernel into one of the
+          // two halves of the register file.)  The waits that it would place are written out: 2 between a vector
+          // instruction's result and a matrix instruction that reads it.
+          f32x16 x = S;
+          if (first)
+            asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(x) : "v"(k), "v"(q));
+          else
+            asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(x) : "v"(k), "v"(q));
+          S = x;
+        } else {
+          S = mma(__builtin_bit_cast(bf16x8, k), q, first ? f32x16{} : S);
         }
-        // the next group but one of places, when its own place is free: looked up here, put there a few intervals later
-        if (i % kPlaces == 2) look_up(i / kPlaces + 2);
-        if (i % kPlaces == kPlaces - 2) put_places(i / kPlaces + 2);
-        lds_barrier();
+      };
+      // The scores of the tile in the registers (its values into `to`, the tile after it into the registers) and, where
+      // SUMS, beside them the sums of the tile in `from` with the weights P.
+      auto products = [&](auto scores_too, auto sums_too, unsigned from, unsigned to) {
+        constexpr bool kScores = decltype(scores_too)::value, kSums = decltype(sums_too)::value;
+        // Steps that the reads of values are ahead.  With one buffer a tile is put where the one before is read: channels
+        // 64 p .. 64 p + 63 (32 p .. 32 p + 31) in steps E p .. E p + E - 1, so those of the E - 1 steps after have to be on their way.
+        constexpr int kFirst = C::kBuffers == 1 ? 4 : 2;
+        static_assert(C::kBuffers > 1 || kFirst >= E);
+        bf16x8 v[kFirst];
+        from = opaque(from);
+        auto read = [&](int e) { return tr_frag(from, at, 16 * (e % 2), e / 2); };
+        if constexpr (kSums) {
+#pragma unroll
+          for (int e = 0; e < kFirst; ++e) v[e] = read(e);
+        }
+        u32x4 k = {};
+        bf16x8 far = {};  // a query from LDS, read ahead
+        if constexpr (kScores) {
+          load_scales();
+          k = channels(0);
+        }
+        const unsigned at_put = opaque(to + put);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          __builtin_amdgcn_sched_barrier(0);
+          u32x4 next = k;
+          if constexpr (kScores) {
+            if (s == 0 && C::far(1)) far = far_query(1);
+            score(k, C::far(s) ? far : qf[s], s == 0);
+            if (s + 2 < KS && C::far(s + 2)) far = far_query(s + 2);
+            if (s + 1 < KS) next = channels(s + 1);
+            if (s / E < kTurn) {
+              const unsigned p = s / E + wq * kTurn;
+              *(lds_u32x4*)(((at_put + 256 * (32 * E * p / 256)) ^ (32 * E * p % 256)) ^ (16 * (s % E))) = k;
+            }
+            if (s % E == E - 1) load_codes(s / E);
+          }
+          if constexpr (kSums) {
+            acc[s / 2] = mma(v[s % kFirst], P[s % 2], acc[s / 2]);
+            if (s + kFirst < KS) v[s % kFirst] = read(s + kFirst);
+          }
+          k = next;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kScores) {
+          bf16x8 q[2];
+          if (C::far(KS) && PS > 0) q[0] = far_query(KS);
+#pragma unroll
+          for (int s = 0; s < PS; ++s) {
+            if (C::far(KS) && s + 1 < PS) q[(s + 1) % 2] = far_query(KS + s + 1);
+            score(in ? pe[s] : u32x4{}, C::far(KS) ? q[s % 2] : qf[KS + s], false);
+            load_key(s);
+          }
+          turn_scales();
+          // the waits between a matrix instruction's result and its use, which the compiler does not place for one written out
+          if constexpr (R == 512) {
+            f32x16 x = S;
+            asm("s_nop 15\n\ts_nop 7" : "+v"(x));
+            S = x;
+          }
+        }
+      };
+      bool passed = false;  // a score is above its reference by more than 2^30
+      unsigned wide = 0;    // a scale of 2^65 or more: the upper two bits of a byte
+      auto highest = [&] {
+        float x = S[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) x = fmaxf(x, S[i]);
+        return x * c;
+      };
+      auto mask = [&](int i) {
+        const int j0 = (t0 + wt + WT * i) * kTile;
+        const unsigned bits = (unsigned)__ballot(in);
+        if (bits == ~0u && j0 + kTile - 1 <= sq.L - sq.Lq + m0 / a.H) return;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!((bits >> acc_row(e, half)) & 1) || j0 + acc_row(e, half) > lim) S[e] = -INFINITY;
+      };
+      auto softmax = [&] {
+        f32x16 p;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          p[i] = kda::fast_exp2(__builtin_fmaf(S[i], c, -m));
+          sum += p[i];
+        }
+        l += sum;
+#pragma unroll
+        for (int i = 0; i < C::kScales; ++i) wide |= next_scale[i] & next_scale[i] << 1;
+        P[0] = acc_frag(p, 0);
+        P[1] = acc_frag(p, 1);
+        passed |= highest() > m + 30.f;
+      };
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      // The first tile into the registers, and the next one's place.
+      auto start = [&] {
+        look_up(0);
+        find();
+        look_up(1);
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) load_codes(p);
+#pragma unroll
+        for (int s = 0; s < PS; ++s) load_key(s);
+        load_scales();
+        turn_scales();
+      };
+      auto step = [&](int i) {  // the tile in the registers becomes the present one, i
+        in = next_in;
+        find();
+        look_up(i + 2);
       };
 
       for (bool again = false;;) {
-        lds_barrier();  // the run before is done with the LDS
-        look_up(0);
-        put_places(0);
-        look_up(1);
-        put_places(1);
-        lds_barrier();
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) bits[e] = fetch(raw[e], place(e));
-        clear(raw[0], bits[0]);
-        scores(raw[0], 0, [] {});
-#pragma unroll
-        for (int r = 0; r < RB; ++r) hand(r, 0);
-        bits[kAhead] = fetch(raw[0], place(kAhead));
-        lds_barrier();
-        f32x4 x[RB];
-        share(0, bits[0], 0, x);
-        if (!again) {
-          float mx[RB];
-#pragma unroll
-          for (int r = 0; r < RB; ++r) mx[r] = highest(x[r]);
-          refer(mx);
+        unsigned from = val, to = C::kBuffers == 2 ? val + C::kVal : val;
+        load_query();
+        start();
+        step(0);
+        products(yes, no, from, from);
+        mask(0);
+        if (!again) m = fmaxf(halves_max(highest()), -FLT_MAX);
+        softmax();
+        for (int i = 1; i < turns; ++i) {
+          if (WQ > 1) lds_barrier();
+          step(i);
+          products(yes, yes, from, to);
+          mask(i);
+          softmax();
+          const unsigned was = from;
+          from = to, to = was;
         }
-#pragma unroll
-        for (int r = 0; r < RB; ++r) softmax(r, x[r], 0);
-        clear(raw[1], bits[1]);
-        scores(raw[1], 1, [] {});
-#pragma unroll
-        for (int r = 0; r < RB; ++r) hand(r, 1);
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) bits[e] = bits[e + 1];
-        bits[kAhead] = fetch(raw[1], place(kAhead + 1));
-        lds_barrier();
-        for (int i = 0; i < count; i += kAhead) {
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k)
-            if (k == 0 || i + k < count) interval(i + k, k);
-        }
+        if (WQ > 1) lds_barrier();
+        products(no, yes, from, to);
         if (again) break;
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          float sum = l[r];  // not finite if any term is not
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(acc[r][d][i], 0.f, sum);
-          passed |= !(fabsf(sum) <= FLT_MAX);
+        again = __any(on && (passed || (wide & 0x80808080u)));
+        if (WQ > 1) {  // the wavefronts' loops have barriers: all do the run again, or none
+          if (lane == 0) flags[wave] = again;
+          lds_barrier();
+          again = uniform((unsigned)(flags[0] | flags[1] | flags[2] | flags[3])) != 0;
+          lds_barrier();
         }
-        if (lane == 0) top[wave][0] = 0.f;
-        if (passed) top[wave][0] = 1.f;
-        lds_barrier();
-        again = uniform(__builtin_bit_cast(unsigned, top[0][0] + top[1][0] + top[2][0] + top[3][0])) != 0;
-        lds_barrier();
         if (!again) break;
-        float mx[RB];
-#pragma unroll
-        for (int r = 0; r < RB; ++r) mx[r] = -INFINITY;
-        for (int t = 0; t < count; ++t) {
-          if (t % kPlaces == 0) {
-            look_up(t / kPlaces);
-            put_places(t / kPlaces);
-            lds_barrier();
-          }
-          const unsigned in = fetch(raw[0], place(t));
-          clear(raw[0], in);
-          scores(raw[0], 0, [] {});
-#pragma unroll
-          for (int r = 0; r < RB; ++r) hand(r, 0);
-          lds_barrier();
-          share(t, in, 0, x);
-#pragma unroll
-          for (int r = 0; r < RB; ++r) mx[r] = fmaxf(mx[r], highest(x[r]));
-          lds_barrier();
+        load_query();
+        start();
+        m = -FLT_MAX;
+        for (int i = 0; i < turns; ++i) {
+          step(i);
+          products(yes, no, val, val);
+          mask(i);
+          m = fmaxf(m, halves_max(highest()));
         }
-        refer(mx);
+        l = 0.f;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          l[r] = 0.f;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) acc[r][d] = f32x16{};
-        }
+        for (int d = 0; d < kOut; ++d) acc[d] = f32x16{};
+        if (WQ > 1) lds_barrier();
       }
     }
 
+    l = halves_sum(l);
+    const int id = lane_id(), row = id & 31, mo = m0 + 32 * wq + row;
+    const bool written = mo < rows;
+    const float mw = m;
+    if constexpr (WT > 1) {  // one reference and sum for the wavefronts of the same rows
+      lds_barrier();  // all are done with the values
+      if (id < 32) top[wave][row] = m, sums[wave][row] = l;
+      lds_barrier();
+      l = 0.f;
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const float x = halves_sum(l[r]);
-      if (half == 0) top[wave][32 * r + l32] = x;
+      for (int t = 0; t < WT; ++t) m = fmaxf(m, top[t * WQ + wq][row]);
+#pragma unroll
+      for (int t = 0; t < WT; ++t) l += sums[t * WQ + wq][row] * kda::fast_exp2(top[t * WQ + wq][row] - m);
     }
-    lds_barrier();
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      float x = 0.f;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) x += top[g][32 * r + l32];
-      l[r] = x;
-    }
-    lds_barrier();  // the next run may write its sums
-    const int ch = wave * CW + 4 * half;
-    const bool first = half == 0 && wave == 0;
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const int mi = m0 + 32 * r + l32;
-      if (mi >= rows) continue;
-      const long long row = (long long)sq.first * a.H + mi;
-      if (whole) {
-        const float f = l[r] == 0.f ? 0.f : 1.f / l[r];  // 0: the row sees nothing
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *(u32x2*)(a.o + row * R + ch + 32 * d + acc_row(i, 0)) =
-                u32x2{kda::pk_bf16(acc[r][d][i] * f, acc[r][d][i + 1] * f),
-                      kda::pk_bf16(acc[r][d][i + 2] * f, acc[r][d][i + 3] * f)};
-        if (a.lse && first) a.lse[row] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * (1.f / kda::kLog2e);
-      } else {
-        const long long to = (long long)slot * C::kRows + 32 * r + l32;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *(f32x4*)(w.po + to * R + ch + 32 * d + acc_row(i, 0)) =
-                f32x4{acc[r][d][i], acc[r][d][i + 1], acc[r][d][i + 2], acc[r][d][i + 3]};
-        if (first) {
-          w.ml[2 * to] = m[r];
-          w.ml[2 * to + 1] = l[r];
-        }
+    const float fw = kda::fast_exp2(mw - m), fo = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees nothing
+    const long long out = (long long)sq.first * a.H + mo, to = (long long)slot * C::kRows + 32 * wq + row;
+    if (written && id < 32 && wt == 0) {
+      if (!whole) {
+        w.ml[2 * to] = m;
+        w.ml[2 * to + 1] = l;
+      } else if (a.lse) {
+        a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kda::kLog2e);
       }
     }
+    bf16* const to_o = a.o + out * R + 4 * (id >> 5);
+    float* const to_part = w.po + to * R + 4 * (id >> 5);
+    auto emit = [&](auto final) {
+      auto write = [&](int d, int i, f32x4 x) {  // 4 channels of the lane's row
+        const int ch = 32 * d + acc_row(i, 0);
+        if constexpr (decltype(final)::value)
+          *(u32x2*)(to_o + ch) = u32x2{kda::pk_bf16(x[0] * fo, x[1] * fo), kda::pk_bf16(x[2] * fo, x[3] * fo)};
+        else
+          *(f32x4*)(to_part + ch) = x;
+      };
+      if constexpr (WT == 1) {
+        if (!written) return;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) write(d, i, f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]});
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        // Each of the WT wavefronts of the same rows sums a share of the channels, in two rounds (the LDS of one tile's
+        // values a wavefront holds half of what the others hand over).  1024 bytes, 16 a lane, a piece of 4 channels.
+        constexpr int kShare = kOut / WT, kRound = kShare * 2;  // 32-channel tiles, pieces a round
+        static_assert(4 * (WT - 1) * kRound * 1024 <= C::kQuery, "the values' LDS holds a round");
+        const unsigned there = lds0 + wq * (WT * (WT - 1) * kRound * 1024) + id * 16;
+        auto mine = [&](int t, int round, int e) {
+          const int x = round * kRound + e, d = t * kShare + x / 4, i = x % 4 * 4;
+          return f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]} * fw;
+        };
+#pragma unroll
+        for (int round = 0; round < 2; ++round) {
+#pragma unroll
+          for (int t = 0; t < WT; ++t)  // to wavefront t, from its ((wt - t) mod WT)-th neighbour
+            if (t != wt) {
+              const unsigned piece = there + (t * (WT - 1) + (wt - t + WT) % WT - 1) * (kRound * 1024);
+#pragma unroll
+              for (int e = 0; e < kRound; ++e) {
+                *(lds_f32x4*)(piece + e * 1024) = mine(t, round, e);
+                if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          lds_barrier();
+#pragma unroll
+          for (int t = 0; t < WT; ++t)
+            if (t == wt && written) {
+#pragma unroll
+              for (int e = 0; e < kRound; ++e) {
+                const int x = round * kRound + e;
+                f32x4 sum = mine(t, round, e);
+#pragma unroll
+                for (int g = 0; g < WT - 1; ++g)
+                  sum += *(lds_f32x4*)(there + (t * (WT - 1) + g) * (kRound * 1024) + e * 1024);
+                write(t * kShare + x / 4, x % 4 * 4, sum);
+                if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          lds_barrier();
+        }
+      }
+    };
+    if (whole)
+      emit(std::true_type{});
+    else
+      emit(std::false_type{});
   }
 }
 
-template <int R, int DR, int RB>
+template <int R, int DR, int WQ>
 hipError_t launch(const PagedWork& w, const Fp4Plan& p, hipStream_t stream) {
-  using C = Fp4<R, DR, RB>;
-  paged_fp4_kernel<R, DR, RB><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w, Divide(w.a.page_size));
+  using C = Fp4<R, DR, WQ>;
+  paged_fp4_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w, Divide(w.a.page_size));
   launch_combine<R, C::kRows, kTile>(w, p.groups, stream);
   return hipGetLastError();
 }
@@ -539,13 +506,11 @@ template <int R, int DR>
 hipError_t launch(const PagedArgs& a, hipStream_t stream) {
   const Fp4Plan p = fp4_plan(a.N, a.Tq, a.H, R, DR, (long long)a.max_pages * a.page_size);
   const PagedWork w = split_work(a, p.space);
-  switch (p.rb) {
+  switch (p.wq) {
     case 1: return launch<R, DR, 1>(w, p, stream);
     case 2: return launch<R, DR, 2>(w, p, stream);
-    case 3: return launch<R, DR, 3>(w, p, stream);
+    default: return launch<R, DR, 4>(w, p, stream);
   }
-  if constexpr (R < 512) return launch<R, DR, 4>(w, p, stream);
-  return hipErrorInvalidValue;
 }
 
 }  // namespace
