@@ -48,12 +48,15 @@ struct Fp4Plan {
   SplitSpace space;
 };
 
+// Workgroups that a CU holds (a wavefront a SIMD each), by their registers.
+constexpr int per_cu(int R, int Dr, int wq) { return R == 512 || (R == 256 && Dr > 0 && wq > 1) ? 1 : 2; }
+
 Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   Fp4Plan p;
   const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
   p.wq = per <= 32 ? 1 : per <= 64 ? 2 : 4;
   const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
-  const long long most = 256, units = blocks * (tiles > 0 ? tiles : 1);
+  const long long most = 256 * per_cu(R, Dr, p.wq), units = blocks * (tiles > 0 ? tiles : 1);
   p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
   p.space = split_space(N, p.groups, 32 * p.wq, R);
   return p;
@@ -93,11 +96,15 @@ struct Fp4 {
   static constexpr int kOut = R / 32;              // 32-channel tiles of O^T
   // A lane's part of a row is loaded in pieces of E steps (E registers of codes), those of the two halves of the lanes
   // side by side: step s = E p + i is of channels 16 E p + 8 E half + 8 i.
-  static constexpr int E = R == 128 ? 2 : 4, kPieces = KS / E, kScales = R / 128;
+  static constexpr int E = R == 512 ? 4 : 2, kPieces = KS / E, kScales = R / 128;
   static constexpr int kTurn = kPieces / WQ;  // the wavefronts of a tile begin so many pieces apart, and put the first
                                               // kTurn of their pieces into LDS for all
   // At R = 512 there are no registers for all of the queries: the rotary part and those of some steps are in LDS.
-  static constexpr bool far(int s) { return R == 512 && (s >= KS || s % 4 == 3 || (WQ != 2 && s % 8 == 1)); }
+  static constexpr bool far(int s) {
+    if (R == 512) return s >= KS || s % 4 == 3 || (WQ != 2 && s % 8 == 1);
+    if (R == 256) return s >= KS ? WQ != 2 : WQ == 1 ? s % 2 == 1 : s % 4 == 3;
+    return false;
+  }
   static constexpr int far_at(int s) {  // 1024 bytes a step
     int n = 0;
     for (int i = 0; i < s; ++i) n += far(i);
@@ -109,7 +116,7 @@ struct Fp4 {
 };
 
 template <int R, int DR, int WQ>
-__global__ __launch_bounds__(256, 1) void paged_fp4_kernel(PagedWork w, Divide by_page) {
+__global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(PagedWork w, Divide by_page) {
   using C = Fp4<R, DR, WQ>;
   constexpr int D = R + DR, KS = C::KS, PS = C::PS, kOut = C::kOut, WT = C::WT, kRow = C::kRow;
   __shared__ __align__(1024) char lds[C::kLds];
@@ -184,8 +191,8 @@ __global__ __launch_bounds__(256, 1) void paged_fp4_kernel(PagedWork w, Divide b
       int page = -1, off = 0;
       bool in = false, next_in = false;
       unsigned long long row = 0, row_end = 0;
-      auto look_up = [&](int i) {  // of tile i: from -1 on all rows are behind the end
-        const int j = (t0 + wt + WT * i) * kTile + l32;
+      auto look_up = [&](int i) {  // of tile i; compared without a sign: it may begin behind all rows that 31 bits count
+        const int j = (t0 + wt + WT * i) * kTile + (lane_id() & 31);
         page = -1;
         if ((unsigned)j < (unsigned)last) {
           const unsigned p = by_page.of(j);
@@ -196,8 +203,9 @@ __global__ __launch_bounds__(256, 1) void paged_fp4_kernel(PagedWork w, Divide b
       auto find = [&] {  // the tile looked up last is the next
         next_in = (unsigned)page < (unsigned)a.num_pages;
         const long long r = next_in ? page * a.page_size + off : 0;
-        row = (unsigned long long)a.cache4 + r * kRow + 4 * E * half;
-        row_end = (unsigned long long)a.cache4 + r * kRow + R / 2 + 16 * half;
+        const int h = lane_id() >> 5;
+        row = (unsigned long long)a.cache4 + r * kRow + 4 * E * h;
+        row_end = (unsigned long long)a.cache4 + r * kRow + R / 2 + 16 * h;
       };
       auto load_codes = [&](int p) {
         const auto from = (global_char*)row + 8 * E * ((p + wq * kTurn) % kPieces);
@@ -210,7 +218,7 @@ __global__ __launch_bounds__(256, 1) void paged_fp4_kernel(PagedWork w, Divide b
       // The scales in the order of the wavefront's pieces: R / 32 bytes, byte p (E = 2) or 2 p + half (E = 4) of piece p.
       constexpr int kBytes = E / 2, kRoll = kBytes * kTurn;
       auto load_scales = [&] {
-        const auto from = (global_char*)row_end - 16 * half + 2 * DR;
+        const auto from = (global_char*)row_end - 16 * (lane_id() >> 5) + 2 * DR;
 #pragma unroll
         for (int i = 0; i < C::kScales; ++i)
           next_scale[i] = *(global_u32*)(from + 4 * ((i + wq * kRoll / 4) % C::kScales));
@@ -252,7 +260,7 @@ __global__ __launch_bounds__(256, 1) void paged_fp4_kernel(PagedWork w, Divide b
         constexpr bool kScores = decltype(scores_too)::value, kSums = decltype(sums_too)::value;
         // Steps that the reads of values are ahead.  With one buffer a tile is put where the one before is read: channels
         // 64 p .. 64 p + 63 (32 p .. 32 p + 31) in steps E p .. E p + E - 1, so those of the E - 1 steps after have to be on their way.
-        constexpr int kFirst = C::kBuffers == 1 ? 4 : 2;
+        constexpr int kFirst = C::kBuffers == 1 ? E : 2;
         static_assert(C::kBuffers > 1 || kFirst >= E);
         bf16x8 v[kFirst];
         from = opaque(from);
@@ -320,9 +328,11 @@ __global__ __launch_bounds__(256, 1) void paged_fp4_kernel(PagedWork w, Divide b
         const int j0 = (t0 + wt + WT * i) * kTile;
         const unsigned bits = (unsigned)__ballot(in);
         if (bits == ~0u && j0 + kTile - 1 <= sq.L - sq.Lq + m0 / a.H) return;
+        const int h = 4 * (lane_id() >> 5), sees = lim - j0 - h;  // rows up to this one, of those from h on
+        const unsigned mine = bits >> h;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (!((bits >> acc_row(e, half)) & 1) || j0 + acc_row(e, half) > lim) S[e] = -INFINITY;
+          if (!((mine >> acc_row(e, 0)) & 1) || acc_row(e, 0) > sees) S[e] = -INFINITY;
       };
       auto softmax = [&] {
         f32x16 p;
