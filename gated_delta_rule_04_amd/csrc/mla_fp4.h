@@ -9,12 +9,14 @@ namespace mla {
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-// 8 codes as 8 bf16, exactly.
+// 2 of 8 codes (codes 2i and 2i + 1) as bf16, exactly, and all 8.
+template <int I>
+__device__ __forceinline__ unsigned fp4_pair(unsigned codes, float scale) {
+  return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));
+}
 __device__ __forceinline__ u32x4 fp4_values(unsigned codes, float scale) {
-  return u32x4{__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0)),
-               __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1)),
-               __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2)),
-               __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3))};
+  return u32x4{fp4_pair<0>(codes, scale), fp4_pair<1>(codes, scale), fp4_pair<2>(codes, scale),
+               fp4_pair<3>(codes, scale)};
 }
 
 }  // namespace mla

@@ -113,6 +113,7 @@ struct Fp4 {
   static constexpr int kVal = kTile * R * 2, kBuffers = WQ == 1 ? 1 : 2;  // bytes of a tile's values, tiles of a group
   static constexpr int kQuery = WT * kBuffers * kVal, kQueries = far_at(KS + PS);
   static constexpr int kLds = kQuery + WQ * kQueries;
+  static constexpr int kPasses = 32 * R * 2 / (kQuery / 4);  // in which the queries go through a quarter of the values' LDS
 };
 
 template <int R, int DR, int WQ>
@@ -171,17 +172,41 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
     if (WQ > 1) lds_barrier();  // the run before is done with the LDS
     if (turns > 0) {
       bf16x8 qf[KS + PS];
-      auto load_query = [&] {  // a row that is not one reads the last again, and is not written
-        const bf16* q = a.q + ((long long)sq.first * a.H + min(m0 + 32 * wq + (lane_id() & 31), rows - 1)) * D;
-        const int h = lane_id() >> 5;
+      // Through LDS (this wavefront's part of the values'), so that each load takes whole rows: 16 bytes a lane from 32
+      // rows would take 64 lines for a sixteenth of each.  A row that is not one reads the last again, and is not written.
+      auto load_query = [&] {
+        constexpr int kPasses = C::kPasses, kRun = kPieces / kPasses, kChunks = 2 * E * kRun, kAt = kChunks * 16;
+        constexpr int kMany = 64 / kChunks;  // rows of a load, if there are several
+        auto place = [](int r) { return kChunks >= 16 ? r & 15 : (r >> 1) & 7; };
+        const int id = lane_id(), first = min(m0 + 32 * wq, rows - 1);
+        const bf16* const q = a.q + ((long long)sq.first * a.H + first) * D;
+        const int end_row = rows - 1 - first;
+        const bf16* const mine = q + min(id & 31, end_row) * D;
 #pragma unroll
-        for (int s = 0; s < KS + PS; ++s) {
-          const int p = (s / E + wq * kTurn) % kPieces;
-          qf[s] = *(const bf16x8*)(s < KS ? q + 16 * E * p + 8 * E * h + 8 * (s % E) : q + R + 16 * (s - KS) + 8 * h);
-          if (C::far(s)) *(lds_u32x4*)(query + C::far_at(s)) = __builtin_bit_cast(u32x4, qf[s]);
-          if (s % 8 == 7) __builtin_amdgcn_sched_barrier(0);  // else more are on their way than there are registers
+        for (int s = 0; s < PS; ++s) qf[KS + s] = *(const bf16x8*)(mine + R + 16 * s + 8 * (id >> 5));
+        const unsigned stage = lds0 + wave * (C::kQuery / 4);
+        const unsigned from_lds = stage + (id & 31) * kAt;
+#pragma unroll
+        for (int pass = 0; pass < kPasses; ++pass) {
+          if (pass > 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+          for (int i = 0; i < 32 / kMany; ++i) {
+            const int r = i * kMany + id / kChunks, chunk = (id % kChunks) ^ place(r);
+            const int p = (chunk / (2 * E) + pass * kRun + wq * kTurn) % kPieces;
+            load_lds(q, (min(r, end_row) * D + 16 * E * p + 8 * (chunk % (2 * E))) * 2, stage + i * 1024);
+          }
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+          for (int s = pass * kRun * E; s < (pass + 1) * kRun * E; ++s) {
+            const int chunk = 2 * E * (s / E - pass * kRun) + s % E;
+            qf[s] = *(const lds_bf16x8*)(from_lds + 16 * ((chunk + E * (id >> 5)) ^ place(id & 31)));
+          }
         }
+#pragma unroll
+        for (int s = 0; s < KS + PS; ++s)
+          if (C::far(s)) *(lds_u32x4*)(query + C::far_at(s)) = __builtin_bit_cast(u32x4, qf[s]);
         __builtin_amdgcn_sched_barrier(0);
+        if (WQ > 1) lds_barrier();  // the values' LDS is all the wavefronts' again
       };
       auto far_query = [&](int s) { return __builtin_bit_cast(bf16x8, *(lds_u32x4*)(query + C::far_at(s))); };
       unsigned code[KS];
@@ -223,21 +248,24 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
         for (int i = 0; i < C::kScales; ++i)
           next_scale[i] = *(global_u32*)(from + 4 * ((i + wq * kRoll / 4) % C::kScales));
       };
-      auto turn_scales = [&] {
+      auto turn_scales = [&] {  // rows that are not there: 2^-127, any finite values
+        const int h = E == 4 ? 8 * (lane_id() >> 5) : 0;
 #pragma unroll
-        for (int i = 0; i < C::kScales; ++i)
-          scale[i] = kRoll % 4 == 0 ? next_scale[i]
-                                    : __builtin_amdgcn_alignbit(next_scale[(i + 1) % C::kScales], next_scale[i],
-                                                                wq * kRoll % 4 * 8);
+        for (int i = 0; i < C::kScales; ++i) {
+          const unsigned x = kRoll % 4 == 0 ? next_scale[i]
+                                            : __builtin_amdgcn_alignbit(next_scale[(i + 1) % C::kScales], next_scale[i],
+                                                                        wq * kRoll % 4 * 8);
+          scale[i] = next_in ? x >> h : 0u;
+        }
       };
 
       f32x16 S;  // S^T of a tile; register i: the lane's row, tile row acc_row(i)
       bf16x8 P[2];
-      // 8 channels of step s, as an A operand.  Rows that are not there have a scale of 2^-127: any finite values.
-      auto channels = [&](int s) {
-        const int byte = kBytes * (s / E);  // and half, where a piece has two
-        const unsigned x = scale[byte / 4] >> (8 * (byte % 4) + (E == 4 ? 8 * half : 0));
-        return fp4_values(code[s], __builtin_bit_cast(float, in ? (x & 255) << 23 : 0u));
+      auto scale_of = [&](int s) {  // step s's, as a float
+        constexpr int kTop = 23;
+        const int at_bit = 8 * (kBytes * (s / E) % 4);
+        const unsigned x = scale[kBytes * (s / E) / 4];
+        return __builtin_bit_cast(float, (at_bit <= kTop ? x << (kTop - at_bit) : x >> (at_bit - kTop)) & 255u << kTop);
       };
       auto score = [&](u32x4 k, bf16x8 q, bool first) {
         if constexpr (R == 512) {
@@ -255,7 +283,8 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
         }
       };
       // The scores of the tile in the registers (its values into `to`, the tile after it into the registers) and, where
-      // SUMS, beside them the sums of the tile in `from` with the weights P.
+      // SUMS, beside them the sums of the tile in `from` with the weights P.  One wavefront issues an instruction every 4
+      // cycles at best (a conversion takes 8) and a product takes 32, so what is between two products is kept even.
       auto products = [&](auto scores_too, auto sums_too, unsigned from, unsigned to) {
         constexpr bool kScores = decltype(scores_too)::value, kSums = decltype(sums_too)::value;
         // Steps that the reads of values are ahead.  With one buffer a tile is put where the one before is read: channels
@@ -263,50 +292,67 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
         constexpr int kFirst = C::kBuffers == 1 ? E : 2;
         static_assert(C::kBuffers > 1 || kFirst >= E);
         bf16x8 v[kFirst];
-        from = opaque(from);
-        auto read = [&](int e) { return tr_frag(from, at, 16 * (e % 2), e / 2); };
+        const unsigned at_from = opaque(from + at.col);
+        auto read = [&](int e) {  // A operand of step e: channels 32 (e / 2) .., rows 16 (e % 2) ..
+          const int d = e / 2, to_tile = 16 * (e % 2) * (R * 2) + 256 * (d / 4);
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)((at_from ^ (64 * (d % 4))) + to_tile));
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4*)((at_from ^ (64 * (d % 4) + 32)) + (to_tile + 8 * (R * 2))));
+          return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
         if constexpr (kSums) {
 #pragma unroll
           for (int e = 0; e < kFirst; ++e) v[e] = read(e);
         }
         u32x4 k = {};
-        bf16x8 far = {};  // a query from LDS, read ahead
+        bf16x8 far = {}, far_key = {};  // queries from LDS, read ahead
+        constexpr int kEvery = PS > 0 ? KS / PS : 1;  // a step of the rotary key after so many of the latent
+        float by = 0.f;
         if constexpr (kScores) {
           load_scales();
-          k = channels(0);
+          by = scale_of(0);
+          k = fp4_values(code[0], by);
+          if (C::far(1)) far = far_query(1);
         }
-        const unsigned at_put = opaque(to + put);
+        constexpr int kShare = 32 * E * kTurn;  // bytes of a row that this wavefront puts
+        const unsigned at_put = opaque(((to + put) ^ (wq * kShare % 256)) + 256 * (wq * kShare / 256));
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          __builtin_amdgcn_sched_barrier(0);
           u32x4 next = k;
+          __builtin_amdgcn_sched_barrier(0);
           if constexpr (kScores) {
-            if (s == 0 && C::far(1)) far = far_query(1);
             score(k, C::far(s) ? far : qf[s], s == 0);
-            if (s + 2 < KS && C::far(s + 2)) far = far_query(s + 2);
-            if (s + 1 < KS) next = channels(s + 1);
-            if (s / E < kTurn) {
-              const unsigned p = s / E + wq * kTurn;
-              *(lds_u32x4*)(((at_put + 256 * (32 * E * p / 256)) ^ (32 * E * p % 256)) ^ (16 * (s % E))) = k;
+            if (s + 1 < KS) {
+              if ((s + 1) % E == 0) by = scale_of(s + 1);
+              next[0] = fp4_pair<0>(code[s + 1], by);
+              next[1] = fp4_pair<1>(code[s + 1], by);
             }
+            if (s / E < kTurn)
+              *(lds_u32x4*)((at_put ^ (32 * E * (s / E) % 256 + 16 * (s % E))) + 256 * (32 * E * (s / E) / 256)) = k;
+            if (PS > 0 && s % kEvery == kEvery / 2 && C::far(KS)) far_key = far_query(KS + s / kEvery);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (kSums) acc[s / 2] = mma(v[s % kFirst], P[s % 2], acc[s / 2]);
+          if constexpr (kScores) {
+            if (s + 1 < KS) {
+              next[2] = fp4_pair<2>(code[s + 1], by);
+              next[3] = fp4_pair<3>(code[s + 1], by);
+            }
+            if (s + 2 < KS && C::far(s + 2)) far = far_query(s + 2);
             if (s % E == E - 1) load_codes(s / E);
           }
-          if constexpr (kSums) {
-            acc[s / 2] = mma(v[s % kFirst], P[s % 2], acc[s / 2]);
+          if constexpr (kSums)
             if (s + kFirst < KS) v[s % kFirst] = read(s + kFirst);
-          }
+          if constexpr (kScores && PS > 0)
+            if (s % kEvery == kEvery - 1) {
+              __builtin_amdgcn_sched_barrier(0);
+              score(pe[s / kEvery], C::far(KS) ? far_key : qf[KS + s / kEvery], false);
+              load_key(s / kEvery);
+            }
           k = next;
         }
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (kScores) {
-          bf16x8 q[2];
-          if (C::far(KS) && PS > 0) q[0] = far_query(KS);
-#pragma unroll
-          for (int s = 0; s < PS; ++s) {
-            if (C::far(KS) && s + 1 < PS) q[(s + 1) % 2] = far_query(KS + s + 1);
-            score(in ? pe[s] : u32x4{}, C::far(KS) ? q[s % 2] : qf[KS + s], false);
-            load_key(s);
-          }
           turn_scales();
           // the waits between a matrix instruction's result and its use, which the compiler does not place for one written out
           if constexpr (R == 512) {
