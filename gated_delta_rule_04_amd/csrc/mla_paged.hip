@@ -88,7 +88,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
 
   Run run;
   Sequence sq;
-  if (!find_run<C::kRows, kTile>(w, run, sq)) return;
+  if (!find_run<C::kRows, kTile>(w, blockIdx.x, run, sq)) return;
   const long long begin = run.begin, end = run.end;
   int n = run.n;
   long long base = run.base;  // units before sequence n

@@ -49,14 +49,14 @@ struct Fp4Plan {
 };
 
 // Workgroups that a CU holds (a wavefront a SIMD each), by their registers.
-constexpr int per_cu(int R, int Dr, int wq) { return R == 512 || (R == 256 && Dr > 0 && wq > 1) ? 1 : 2; }
+constexpr int per_cu(int R, int wq) { return R == 512 || (R == 256 && wq > 1) ? 1 : 2; }
 
 Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   Fp4Plan p;
   const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
   p.wq = per <= 32 ? 1 : per <= 64 ? 2 : 4;
   const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
-  const long long most = 256 * per_cu(R, Dr, p.wq), units = blocks * (tiles > 0 ? tiles : 1);
+  const long long most = 256 * per_cu(R, p.wq), units = blocks * (tiles > 0 ? tiles : 1);
   p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
   p.space = split_space(N, p.groups, 32 * p.wq, R);
   return p;
@@ -96,13 +96,13 @@ struct Fp4 {
   static constexpr int kOut = R / 32;              // 32-channel tiles of O^T
   // A lane's part of a row is loaded in pieces of E steps (E registers of codes), those of the two halves of the lanes
   // side by side: step s = E p + i is of channels 16 E p + 8 E half + 8 i.
-  static constexpr int E = R == 512 ? 4 : 2, kPieces = KS / E, kScales = R / 128;
+  static constexpr int E = R == 512 || (R == 256 && WQ > 1) ? 4 : 2, kPieces = KS / E, kScales = R / 128;
   static constexpr int kTurn = kPieces / WQ;  // the wavefronts of a tile begin so many pieces apart, and put the first
                                               // kTurn of their pieces into LDS for all
   // At R = 512 there are no registers for all of the queries: the rotary part and those of some steps are in LDS.
   static constexpr bool far(int s) {
     if (R == 512) return s >= KS || s % 4 == 3 || (WQ != 2 && s % 8 == 1);
-    if (R == 256) return s >= KS ? WQ != 2 : WQ == 1 ? s % 2 == 1 : s % 4 == 3;
+    if (R == 256) return WQ == 1 && (s >= KS || s % 2 == 1);
     return false;
   }
   static constexpr int far_at(int s) {  // 1024 bytes a step
@@ -117,7 +117,7 @@ struct Fp4 {
 };
 
 template <int R, int DR, int WQ>
-__global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(PagedWork w, Divide by_page) {
+__global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork w, Divide by_page) {
   using C = Fp4<R, DR, WQ>;
   constexpr int D = R + DR, KS = C::KS, PS = C::PS, kOut = C::kOut, WT = C::WT, kRow = C::kRow;
   __shared__ __align__(1024) char lds[C::kLds];
@@ -128,7 +128,10 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wt = wave / WQ;
   Run run;
   Sequence sq;
-  if (!find_run<C::kRows, kTile>(w, run, sq)) return;
+  // Workgroups go round the 8 XCDs: neighbours in the work, which share queries or cache rows, are put on one.
+  const int xcd = blockIdx.x % 8, each = gridDim.x / 8, over = gridDim.x % 8;
+  const int group = xcd * each + min(xcd, over) + blockIdx.x / 8;
+  if (!find_run<C::kRows, kTile>(w, group, run, sq)) return;
   // The same in all lanes, and said so: what follows from them stays in scalar registers.
   const long long begin = uniform((unsigned long long)run.begin), end = uniform((unsigned long long)run.end);
   long long base = uniform((unsigned long long)run.base);  // units before sequence n
@@ -150,7 +153,7 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
     const int block = (int)((u - base) / sq.tiles), t0 = (int)((u - base) % sq.tiles);
     const int t1 = (int)min((long long)sq.tiles, t0 + (end - u));
     const bool whole = t0 == 0 && t1 == sq.tiles;
-    const int slot = 2 * blockIdx.x + (u == begin ? 0 : 1);
+    const int slot = 2 * group + (u == begin ? 0 : 1);
     u += t1 - t0;
     const int rows = sq.Lq * a.H, m0 = block * C::kRows;
     // the last cache row that a row of the block sees
@@ -407,7 +410,6 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
 #pragma unroll
         for (int s = 0; s < PS; ++s) load_key(s);
         load_scales();
-        turn_scales();
       };
       auto step = [&](int i) {  // the tile in the registers becomes the present one, i
         in = next_in;
@@ -417,8 +419,9 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
 
       for (bool again = false;;) {
         unsigned from = val, to = C::kBuffers == 2 ? val + C::kVal : val;
-        load_query();
         start();
+        load_query();
+        turn_scales();
         step(0);
         products(yes, no, from, from);
         mask(0);
@@ -444,8 +447,9 @@ __global__ __launch_bounds__(256, per_cu(R, DR, WQ)) void paged_fp4_kernel(Paged
           lds_barrier();
         }
         if (!again) break;
-        load_query();
         start();
+        load_query();
+        turn_scales();
         m = -FLT_MAX;
         for (int i = 0; i < turns; ++i) {
           step(i);

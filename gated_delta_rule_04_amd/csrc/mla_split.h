@@ -46,10 +46,10 @@ struct Run {
   long long begin, end;
 };
 
-// Finds the run of this workgroup (256 threads) and its first sequence; false when there is none.  Workgroup 0 writes
+// Finds the run of workgroup `group` (256 threads) and its first sequence; false when there is none.  Workgroup 0 writes
 // the sequences' prefix for the join.
 template <int ROWS, int TILE>
-__device__ __forceinline__ bool find_run(const PagedWork& w, Run& run, Sequence& sq) {
+__device__ __forceinline__ bool find_run(const PagedWork& w, int group, Run& run, Sequence& sq) {
   constexpr int kWaves = 4, kThreads = 64 * kWaves;
   __shared__ long long scan[kWaves + 1];
   __shared__ long long found[2];
@@ -79,12 +79,12 @@ __device__ __forceinline__ bool find_run(const PagedWork& w, Run& run, Sequence&
     const int n = n0 + tid;
     mine = n < a.N ? sequence<ROWS, TILE>(a, n).units() : 0;
     incl = block_scan(mine) + total;
-    if (blockIdx.x == 0 && n < a.N) w.prefix[n] = incl - mine;
+    if (group == 0 && n < a.N) w.prefix[n] = incl - mine;
     total += scan[kWaves];
   }
-  if (blockIdx.x == 0 && tid == 0) w.prefix[a.N] = total;
+  if (group == 0 && tid == 0) w.prefix[a.N] = total;
   const long long share = (total + gridDim.x - 1) / gridDim.x;
-  run.begin = share * blockIdx.x;
+  run.begin = share * group;
   run.end = min(run.begin + share, total);
   if (run.begin >= run.end) return false;
   long long before = 0;
