@@ -18,9 +18,9 @@
 //
 // The exponentials of a row have one reference through a run of tiles, the largest
 // score of the first: bf16 weights and float32 sums lose nothing by a reference
-// that is below the row's largest score by 2^30, while values stay below 2^68 (the
-// sums of 2^27 of them below 2^125).  Where a score passes it by more, or a scale
-// is 2^65 or more, the run is done again with the largest score of all its tiles,
+// that is below the row's largest score by 2^60, while values stay below 2^36 (the
+// sums of 2^27 of them below 2^123).  Where a score passes it by more, or a scale
+// is 2^33 or more, the run is done again with the largest score of all its tiles,
 // found first; so a run takes three passes at most, and the loop has no rescaling
 // of the sums, which would cost them their place in the accumulators.
 
@@ -54,7 +54,9 @@ constexpr int per_cu(int R, int wq) { return R == 512 || (R == 256 && wq > 1) ? 
 Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   Fp4Plan p;
   const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
-  p.wq = per <= 32 ? 1 : per <= 64 ? 2 : 4;
+  auto padded = [&](int block) { return (per + block - 1) / block * block; };
+  auto good = [&](int block) { return rows / block >= 256 && 8 * padded(block) <= 9 * padded(32); };
+  p.wq = good(128) ? 4 : good(64) ? 2 : 1;
   const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
   const long long most = 256 * per_cu(R, p.wq), units = blocks * (tiles > 0 ? tiles : 1);
   p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
@@ -178,6 +180,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
       // Through LDS (this wavefront's part of the values'), so that each load takes whole rows: 16 bytes a lane from 32
       // rows would take 64 lines for a sixteenth of each.  A row that is not one reads the last again, and is not written.
       auto load_query = [&] {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what this wavefront put there last is there
         constexpr int kPasses = C::kPasses, kRun = kPieces / kPasses, kChunks = 2 * E * kRun, kAt = kChunks * 16;
         constexpr int kMany = 64 / kChunks;  // rows of a load, if there are several
         auto place = [](int r) { return kChunks >= 16 ? r & 15 : (r >> 1) & 7; };
@@ -365,8 +368,8 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
           }
         }
       };
-      bool passed = false;  // a score is above its reference by more than 2^30
-      unsigned wide = 0;    // a scale of 2^65 or more: the upper two bits of a byte
+      bool passed = false;  // a score is above its reference by more than 2^60
+      unsigned wide = 0;    // a scale of 2^33 or more: bit 7 of a byte and one of the two below
       auto highest = [&] {
         float x = S[0];
 #pragma unroll
@@ -393,10 +396,10 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         }
         l += sum;
 #pragma unroll
-        for (int i = 0; i < C::kScales; ++i) wide |= next_scale[i] & next_scale[i] << 1;
+        for (int i = 0; i < C::kScales; ++i) wide |= next_scale[i] & (next_scale[i] << 1 | next_scale[i] << 2);
         P[0] = acc_frag(p, 0);
         P[1] = acc_frag(p, 1);
-        passed |= highest() > m + 30.f;
+        passed |= highest() > m + 60.f;
       };
       constexpr std::true_type yes{};
       constexpr std::false_type no{};
@@ -467,8 +470,14 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
     l = halves_sum(l);
     const int id = lane_id(), row = id & 31, mo = m0 + 32 * wq + row;
     const bool written = mo < rows;
-    const float mw = m;
-    if constexpr (WT > 1) {  // one reference and sum for the wavefronts of the same rows
+    // The sums of a row are handed on in units in which its l is near 1 (scaled by a power of two, exactly): with the
+    // run's own reference, far below the row's largest score, what scales them later would leave the range of float32
+    // where they, larger than 1, have not.
+    const int size = __builtin_amdgcn_frexp_expf(l);
+    m += (float)size;
+    l = ldexpf(l, -size);
+    float f[WT] = {1.f};
+    if constexpr (WT > 1) {  // one reference and sum for the wavefronts of the same rows; f: their factors, from this one on
       lds_barrier();  // all are done with the values
       if (id < 32) top[wave][row] = m, sums[wave][row] = l;
       lds_barrier();
@@ -477,8 +486,10 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
       for (int t = 0; t < WT; ++t) m = fmaxf(m, top[t * WQ + wq][row]);
 #pragma unroll
       for (int t = 0; t < WT; ++t) l += sums[t * WQ + wq][row] * kda::fast_exp2(top[t * WQ + wq][row] - m);
+#pragma unroll
+      for (int t = 0; t < WT; ++t) f[t] = kda::fast_exp2(top[(wt + t) % WT * WQ + wq][row] - m);
     }
-    const float fw = kda::fast_exp2(mw - m), fo = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees nothing
+    const float fo = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees nothing
     const long long out = (long long)sq.first * a.H + mo, to = (long long)slot * C::kRows + 32 * wq + row;
     if (written && id < 32 && wt == 0) {
       if (!whole) {
@@ -491,6 +502,10 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
     bf16* const to_o = a.o + out * R + 4 * (id >> 5);
     float* const to_part = w.po + to * R + 4 * (id >> 5);
     auto emit = [&](auto final) {
+      auto shifted = [&](int d, int i) {
+        return f32x4{ldexpf(acc[d][i], -size), ldexpf(acc[d][i + 1], -size), ldexpf(acc[d][i + 2], -size),
+                     ldexpf(acc[d][i + 3], -size)};
+      };
       auto write = [&](int d, int i, f32x4 x) {  // 4 channels of the lane's row
         const int ch = 32 * d + acc_row(i, 0);
         if constexpr (decltype(final)::value)
@@ -503,7 +518,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
 #pragma unroll
         for (int d = 0; d < kOut; ++d) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) write(d, i, f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]});
+          for (int i = 0; i < 16; i += 4) write(d, i, shifted(d, i));
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
@@ -514,7 +529,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         const unsigned there = lds0 + wq * (WT * (WT - 1) * kRound * 1024) + id * 16;
         auto mine = [&](int t, int round, int e) {
           const int x = round * kRound + e, d = t * kShare + x / 4, i = x % 4 * 4;
-          return f32x4{acc[d][i], acc[d][i + 1], acc[d][i + 2], acc[d][i + 3]} * fw;
+          return shifted(d, i);
         };
 #pragma unroll
         for (int round = 0; round < 2; ++round) {
@@ -535,10 +550,10 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
 #pragma unroll
               for (int e = 0; e < kRound; ++e) {
                 const int x = round * kRound + e;
-                f32x4 sum = mine(t, round, e);
+                f32x4 sum = mine(t, round, e) * f[0];
 #pragma unroll
                 for (int g = 0; g < WT - 1; ++g)
-                  sum += *(lds_f32x4*)(there + (t * (WT - 1) + g) * (kRound * 1024) + e * 1024);
+                  sum += *(lds_f32x4*)(there + (t * (WT - 1) + g) * (kRound * 1024) + e * 1024) * f[g + 1];
                 write(t * kShare + x / 4, x % 4 * 4, sum);
                 if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
               }
