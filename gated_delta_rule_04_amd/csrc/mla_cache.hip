@@ -20,6 +20,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 
+typedef __attribute__((address_space(1))) const u32x4 global_u32x4;
+typedef __attribute__((address_space(1))) const unsigned global_u32;
+typedef __attribute__((address_space(1))) const unsigned char global_u8;
+typedef __attribute__((address_space(1))) const char global_char;
+
 __device__ __forceinline__ bool kept(const AppendArgs& a, int t, int& slot) {
   slot = a.slots[t];
   return (unsigned)slot < (unsigned)a.num_slots;
@@ -190,45 +195,83 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int late
   }
 }
 
-// Rows of a 4-bit cache as bf16: R / 8 lanes a row, 8 channels a lane (4 bytes in,
-// 16 out), the rotary key by the first 8 of them.
+// The last n in [0, N) whose clamped start is not above t, 64 candidates a step; the same for all lanes.
+__device__ __forceinline__ int starts_before(const GatherArgs& a, long long t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = a.N;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64, i = lo + lane * step;
+    const int count = __popcll(__ballot(i < hi && min(max(a.cu[i], 0), a.T) <= t));
+    lo += max(count - 1, 0) * step;
+    hi = min(lo + step, hi);
+  }
+  return lo;
+}
+
+// Rows of a 4-bit cache as bf16.  A wavefront takes kGather rows: first a lane
+// finds each row's place (sequence, page), then R / 8 lanes a row read the
+// latent, 8 channels a lane (4 bytes in, 16 out), and 8 lanes a row the rotary
+// key, all rows at once.  A row that is not there reads the first one (of the
+// output, if the cache has none) and is put as zeros: without a branch, all
+// loads are on their way together.
+constexpr int kGather = 8;
+
 template <int R, int DR>
 __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
-  constexpr int kLanes = R / 8, kRows = kThreads / kLanes, kRow = fp4_row_bytes(R, DR);
-  const long long t = (long long)blockIdx.x * kRows + threadIdx.x / kLanes;
-  const int c = threadIdx.x % kLanes;
-  if (t >= min(max(a.cu[a.N], 0), a.T)) return;
-  int lo = 0, hi = a.N;
-  while (hi - lo > 1) {  // the last sequence that starts at or before the row
-    const int mid = lo + (hi - lo) / 2;
-    if (min(max(a.cu[mid], 0), a.T) <= t)
-      lo = mid;
-    else
-      hi = mid;
+  constexpr int kLanes = R / 8, kOnce = 64 / kLanes, kTimes = kGather / kOnce, kRow = fp4_row_bytes(R, DR);
+  static_assert(DR == 0 || DR / 8 * kGather == 64, "8 rows' rotary keys in one load");
+  const int lane = threadIdx.x & 63, c = lane % kLanes;
+  const long long t0 = ((long long)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)) * kGather;
+  const int count = (int)(min(t0 + kGather, (long long)min(max(a.cu[a.N], 0), a.T)) - t0);
+  if (count <= 0) return;
+  const int first = starts_before(a, t0), last = starts_before(a, t0 + count - 1);
+  int place = -1;
+  if (lane < count) {
+    const long long t = t0 + lane;
+    int lo = first, hi = last + 1;
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (min(max(a.cu[mid], 0), a.T) <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const long long j = t - min(max(a.cu[lo], 0), a.T) + (a.starts ? a.starts[lo] : 0);
+    if (j >= 0 && j < (long long)a.max_pages * a.page_size) {
+      const unsigned p = (unsigned)j / (unsigned)a.page_size;
+      const int page = a.table[(long long)lo * a.max_pages + p];
+      if ((unsigned)page < (unsigned)a.num_pages) place = page * a.page_size + (int)((unsigned)j - p * a.page_size);
+    }
   }
-  const long long j = t - min(max(a.cu[lo], 0), a.T) + (a.starts ? a.starts[lo] : 0);
-  const unsigned char* row = nullptr;
-  if (j >= 0 && j < (long long)a.max_pages * a.page_size) {
-    const unsigned p = (unsigned)j / (unsigned)a.page_size;
-    const int page = a.table[(long long)lo * a.max_pages + p];
-    if ((unsigned)page < (unsigned)a.num_pages)
-      row = a.cache + ((long long)page * a.page_size + ((unsigned)j - p * a.page_size)) * kRow;
+  const auto cache = (global_char*)(a.num_pages > 0 ? a.cache : (const unsigned char*)a.rows);
+  auto row = [&](int i) { return cache + (long long)max(i, 0) * kRow; };
+  const int pe_row = lane / 8, pe_place = __shfl(place, pe_row);
+  u32x4 pe = {};
+  if constexpr (DR > 0) pe = *(global_u32x4*)(row(pe_place) + R / 2 + 16 * (lane % 8));
+  unsigned codes[kTimes], scale[kTimes];
+  bool there[kTimes];
+#pragma unroll
+  for (int i = 0; i < kTimes; ++i) {
+    const int at = __shfl(place, i * kOnce + lane / kLanes);
+    there[i] = at >= 0;
+    codes[i] = *(global_u32*)(row(at) + 4 * c);
+    scale[i] = *(global_u8*)(row(at) + R / 2 + 2 * DR + c / 4);
   }
-  u32x4 v = {}, pe = {};
-  if (row) {
-    const unsigned codes = *(const unsigned*)(row + 4 * c);
-    v = fp4_values(codes, __builtin_bit_cast(float, (unsigned)row[R / 2 + 2 * DR + c / 4] << 23));
-    if (DR && c < DR / 8) pe = *(const u32x4*)(row + R / 2 + 16 * c);
+  bf16* const out = a.rows + t0 * (R + DR);
+#pragma unroll
+  for (int i = 0; i < kTimes; ++i) {
+    const int r = i * kOnce + lane / kLanes;
+    const u32x4 v = fp4_values(codes[i], __builtin_bit_cast(float, scale[i] << 23));
+    if (r < count) *(u32x4*)(out + r * (R + DR) + 8 * c) = there[i] ? v : u32x4{};
   }
-  bf16* out = a.rows + t * (R + DR);
-  *(u32x4*)(out + 8 * c) = v;
-  if (DR && c < DR / 8) *(u32x4*)(out + R + 8 * c) = pe;
+  if constexpr (DR > 0)
+    if (pe_row < count) *(u32x4*)(out + pe_row * (R + DR) + R + 8 * (lane % 8)) = pe_place >= 0 ? pe : u32x4{};
 }
 
 template <int R, int DR>
 hipError_t launch_gather(const GatherArgs& a, hipStream_t stream) {
-  constexpr int kRows = kThreads / (R / 8);
-  gather_kernel<R, DR><<<dim3((unsigned)((a.T + kRows - 1) / kRows)), dim3(kThreads), 0, stream>>>(a);
+  constexpr int kRows = kThreads / 64 * kGather;
+  gather_kernel<R, DR><<<dim3((unsigned)(((long long)a.T + kRows - 1) / kRows)), dim3(kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -175,8 +175,9 @@ def _paged(name, fp4, need, q, cache, block_table, seq_lens, latent_dim, scale, 
         raise ValueError("q must be [N, H, R + Dr], one token a sequence, without cu_seqlens")
     dt, i32 = q.dtype, torch.int32
     dev = _check(q, (cache, "cache", (num_pages, page_size, row), torch.uint8 if fp4 else dt),
-                 (block_table, "block_table", None, i32), (seq_lens, "seq_lens", (N,), i32), (cu_seqlens, "cu_seqlens", (N + 1,), i32),
-                 (out, "out", (Tq, H, R), dt), (lse, "lse", (Tq, H), torch.float32))
+                 (block_table, "block_table", None, i32), (seq_lens, "seq_lens", (N,), i32),
+                 (cu_seqlens, "cu_seqlens", (N + 1,), i32), (out, "out", (Tq, H, R), dt),
+                 (lse, "lse", (Tq, H), torch.float32))
     code = _dt(q)
     if not 0 <= R <= D:
         raise ValueError("latent_dim must be within q's width")
@@ -240,13 +241,27 @@ def cache_gather_fp4(cache, block_table, cu_seqlens, num_tokens, latent_dim, sta
     return out
 
 
-def _outputs(out, shapes, dev):
-    """The given int32 outputs, and new ones in the place of those that are not."""
-    unknown = () if out is None else set(out) - set(shapes)
+def _outputs(out, sizes, workspace, need, dev):
+    """The given int32 outputs, and new ones in the place of those that are not, and the workspace with its size.  What
+    is new is one allocation (7 of them took 9 us of a 20 us call)."""
+    out = out or {}
+    unknown = set(out) - set(sizes)
     if unknown:
         raise ValueError("unknown outputs: %s" % ", ".join(sorted(unknown)))
-    got = {n: None if out is None else out.get(n) for n in shapes}
-    return {n: torch.empty(shapes[n], dtype=torch.int32, device=dev) if t is None else t for n, t in got.items()}
+    new = [n for n in sizes if out.get(n) is None]
+    if workspace is not None:
+        workspace, nbytes = _workspace(workspace, 0, dev)
+        ws = ()
+    else:
+        nbytes, ws = need, (need // 4,)
+    parts = ()
+    if ws or new:
+        lengths = [*ws, *(sizes[n] for n in new)]
+        parts = torch.empty(sum(lengths), dtype=torch.int32, device=dev).split(lengths)
+        if ws:
+            workspace, parts = parts[0], parts[1:]
+    got = dict(zip(new, parts))
+    return {n: got[n] if n in got else out[n] for n in sizes}, workspace, nbytes
 
 
 def cache_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, num_tokens, out=None, workspace=None):
@@ -269,14 +284,12 @@ def cache_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_siz
     if T < 0:
         raise ValueError("num_tokens must not be negative")
     i32 = torch.int32
-    shapes = {"cu_seqlens": (N + 1,), "positions": (T,), "slots": (T,), "kv_lens": (N,), "seq_lens": (N,),
-              "free_count": (1,)}
+    sizes = {"cu_seqlens": N + 1, "positions": T, "slots": T, "kv_lens": N, "seq_lens": N, "free_count": 1}
     dev = _check(block_table, (block_table, "block_table", None, i32), (new_lens, "new_lens", (N,), i32),
                  (seq_lens, "seq_lens", (N,), i32), (free_pages, "free_pages", None, i32),
                  (free_count, "free_count", (1,), i32),
-                 *((t, "out[%r]" % n, shapes[n], i32) for n, t in (out or {}).items() if n in shapes))
-    o = _outputs(out, shapes, dev)
-    ws, nbytes = _workspace(workspace, 0 if workspace is not None else _plan_bytes("plan", N), dev)
+                 *((t, "out[%r]" % n, (sizes[n],), i32) for n, t in (out or {}).items() if n in sizes))
+    o, ws, nbytes = _outputs(out, sizes, workspace, _plan_bytes("plan", N), dev)
     _call("kda_mla_cache_plan", dev, _ptr(new_lens), _ptr(seq_lens), _ptr(block_table), _ptr(free_pages),
           _ptr(free_count), free_pages.numel(), _ptr(o["cu_seqlens"]), _ptr(o["positions"]), _ptr(o["slots"]),
           _ptr(o["kv_lens"]), _ptr(o["seq_lens"]), _ptr(o["free_count"]), N, T, int(page_size), max_pages, _ptr(ws),
@@ -296,13 +309,12 @@ def cache_release(finished, seq_lens, block_table, free_pages, free_count, page_
         raise ValueError("block_table must be [N, max_pages], free_pages [num_free]")
     N, max_pages = block_table.shape
     i32 = torch.int32
-    shapes = {"seq_lens": (N,), "free_count": (1,)}
+    sizes = {"seq_lens": N, "free_count": 1}
     dev = _check(block_table, (block_table, "block_table", None, i32), (finished, "finished", (N,), torch.bool),
                  (seq_lens, "seq_lens", (N,), i32), (free_pages, "free_pages", None, i32),
                  (free_count, "free_count", (1,), i32),
-                 *((t, "out[%r]" % n, shapes[n], i32) for n, t in (out or {}).items() if n in shapes))
-    o = _outputs(out, shapes, dev)
-    ws, nbytes = _workspace(workspace, 0 if workspace is not None else _plan_bytes("release", N), dev)
+                 *((t, "out[%r]" % n, (sizes[n],), i32) for n, t in (out or {}).items() if n in sizes))
+    o, ws, nbytes = _outputs(out, sizes, workspace, _plan_bytes("release", N), dev)
     _call("kda_mla_cache_release", dev, _ptr(finished), _ptr(seq_lens), _ptr(block_table), _ptr(free_pages),
           _ptr(free_count), free_pages.numel(), _ptr(o["seq_lens"]), _ptr(o["free_count"]), N, int(page_size), max_pages,
           _ptr(ws), nbytes)
