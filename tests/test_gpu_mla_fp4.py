@@ -389,6 +389,76 @@ def test_paged_fp4_long_runs_of_chunks(R, Dr):
     _check_all_rows("chunks R%d" % R, *marked(91 + R, lens, 24, 16, R, Dr, q_lens=q_lens, pool=9), R, 0.1)
 
 
+def _tokens(height, H, N, seed):
+    """New tokens a sequence, enough of them for blocks of `height` rows: 256 blocks or more in all."""
+    r = np.random.default_rng(seed)
+    q_lens = r.integers(1, 2 * 300 * height // (H * N), N)
+    q_lens[1] = 0
+    while int(q_lens.sum()) * H < 256 * height:
+        q_lens[2] += 1
+    assert int(q_lens.sum()) * H < 512 * height
+    return q_lens
+
+
+@pytest.mark.parametrize("height", [64, 128])
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_blocks_of_more_rows(R, Dr, height):
+    """Many rows a sequence: longer caches, first chunks, rows that see nothing, an empty sequence, a last block in part."""
+    print("CASE blocks", R, Dr, height, flush=True)
+    r = np.random.default_rng(R + Dr + height)
+    q_lens = _tokens(height, 61, 9, height + R)
+    lens = q_lens + r.integers(0, 700, 9)
+    lens[0], lens[3], lens[4] = q_lens[0], q_lens[3] // 2, 0
+    _check_all_rows("blocks of %d R%d" % (height, R), *marked(111 + R, lens, 24, 61, R, Dr, q_lens=q_lens, pool=9), R, 0.1)
+
+
+@pytest.mark.parametrize("height", [64, 128])
+@pytest.mark.parametrize("R,Dr", [(512, 64), (256, 0), (128, 64)])
+def test_paged_fp4_blocks_of_more_rows_with_missing_pages(R, Dr, height):
+    print("CASE blocks, missing", R, Dr, height, flush=True)
+    q_lens = _tokens(height, 64, 8, height)
+    q, cache, table, lens, cu = marked(121 + R, q_lens + 400, 16, 64, R, Dr, q_lens=q_lens, pool=9)
+    r = np.random.default_rng(height)
+    gone = r.random(table.shape) < 0.1
+    gone[:, :3] |= r.random((len(lens), 3)) < 0.5  # the first tiles have fewer rows, or none
+    gone[2, :8], gone[5] = True, True
+    table[gone] = r.choice([-1, cache.shape[0], 1 << 30], int(gone.sum()))
+    _check_all_rows("missing, blocks of %d" % height, q, cache, table, lens, cu, R, 0.1)
+
+
+@pytest.mark.parametrize("height", [32, 64, 128])
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_scores_far_above_the_first(R, Dr, height):
+    """Rows whose largest score is more than 2^60 above those of their first cache rows, rows where it is not, and rows
+    whose first cache rows are not there."""
+    print("CASE far above", R, Dr, height, flush=True)
+    N, H = 8, 64
+    q_lens = np.array([1, 2, 1, 1, 3, 1, 1, 1]) if height == 32 else _tokens(height, H, N, height + 1)
+    q, cache, table, lens, cu = marked(131 + R, q_lens + 900, 16, H, R, Dr, q_lens=q_lens, pool=60, rise=(0.01, 4.0))
+    scale = 200.0 / (R + Dr)
+    q[cu[3]:cu[4]] *= 0.1                 # scores near each other
+    table[6, :5] = -1
+    first, late = [], []
+    for n in (0, 4):
+        k = torch.from_numpy(in_fp4(cache, R)[1])[torch.as_tensor(table[n]).long()].reshape(-1, R + Dr)[:int(lens[n])]
+        s = q[cu[n]].double() @ k.T * scale / np.log(2)
+        first.append(s[:, :32].amax(1)), late.append(s.amax(1))
+    assert bool((torch.cat(late) - torch.cat(first) > 60).any())
+    _check_all_rows("far above, blocks of %d" % height, q, cache, table, lens, cu, R, scale)
+
+
+@pytest.mark.parametrize("height", [64, 128])
+def test_paged_fp4_large_scales_in_blocks_of_more_rows(height):
+    """Latents up to 2^60, the queries the other way round."""
+    R, Dr, H = 512, 64, 64
+    q_lens = _tokens(height, H, 8, height + 2)
+    q, cache, table, lens, cu = marked(141, q_lens + 300, 16, H, R, Dr, q_lens=q_lens, pool=9)
+    up = torch.exp2(torch.linspace(-60, 60, R // 32).round()).repeat_interleave(32)
+    cache[..., :R] = (cache[..., :R].float() * up).to(BF16)
+    q[..., :R] = (q[..., :R].float() / up).to(BF16)
+    _check_all_rows("large scales, blocks of %d" % height, q, cache, table, lens, cu, R, 0.02)
+
+
 @pytest.mark.parametrize("R,Dr,H,lens", [(128, 0, 8, [20000]), (512, 64, 12, [131072]), (256, 0, 64, [70000, 900]),
                                          (512, 64, 96, [30000, 0, 41000])])
 def test_paged_fp4_every_part_of_a_long_cache(R, Dr, H, lens):
