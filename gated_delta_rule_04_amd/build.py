@@ -50,9 +50,6 @@ SOURCE_FLAGS = {
     # channels take 380 registers, not 339.
     "mla_paged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "mla_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-    # The same for the 4-bit paged attention (512 channels, 96 rows: 209 spills
-    # without); with the target's own register-pressure trackers it takes 481 registers.
-    "mla_paged_fp4.hip": [],
 }
 
 

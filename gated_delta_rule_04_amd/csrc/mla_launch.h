@@ -75,6 +75,7 @@ struct PagedArgs {
   int N, Tq, H, num_pages, page_size, max_pages;
   float scale;
   void* ws;
+  int start = 0;  // what beginning a block of rows costs, in tiles, where the work is cut evenly
 };
 size_t paged_workspace(int N, int Tq, int H, int R, int Dr, long long max_len);
 hipError_t launch_paged(int R, int Dr, const PagedArgs& a, hipStream_t stream);

@@ -33,6 +33,12 @@ namespace mla {
 namespace {
 
 constexpr int kTile = 32;  // cache rows of a tile
+// Beginning a block (queries, first loads, handing the sums on) costs a workgroup as much as about 12 / WQ tiles.
+// Counted so where the work is cut, it keeps workgroups with the ends of short sequences from being the last (N64 H96
+// to 8,192 rows of 512 + 64: 118 us without, 111 with, N256 H8 to 2,048 rows of 256: 37 and 33; where all ends fall on
+// cuts, N256 H8 R256 of 2,048 each, it loses: 34 and 37).  Not where blocks are few and most workgroups have a part of
+// one.
+constexpr int kStart = 12;
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
@@ -45,21 +51,29 @@ typedef __attribute__((address_space(1))) const char global_char;
 struct Fp4Plan {
   int wq;      // wavefronts of 32 rows in a block
   int groups;  // workgroups
+  int start;   // PagedArgs::start
   SplitSpace space;
 };
 
-// Workgroups that a CU holds (a wavefront a SIMD each), by their registers.
+// Workgroups that a CU holds (a wavefront a SIMD each), by their registers.  256 channels: in blocks of 32 rows two
+// with pieces of two steps fill each other's waits in short runs (N256 H8 to 2,048: 35 us, one with pieces of four 44;
+// in long ones, of 8,192, 116 and 104); in taller blocks one with all queries in registers (N256 H128 of 8,192: 305
+// us, two 381).
 constexpr int per_cu(int R, int wq) { return R == 512 || (R == 256 && wq > 1) ? 1 : 2; }
 
 Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   Fp4Plan p;
   const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
-  auto padded = [&](int block) { return (per + block - 1) / block * block; };
-  auto good = [&](int block) { return rows / block >= 256 && 8 * padded(block) <= 9 * padded(32); };
+  // Taller blocks convert and put a tile for fewer rows each and read the cache less often (4 chunks of 512 tokens, 96
+  // heads of 512 + 64: 1.98 ms with 128 rows, 2.1 with 64, 2.4 with 32); lower ones cut evenly and pad less (N64 H96 to
+  // 8,192: 122 us with 32 rows, 137 with 64, 139 with 128).  So the tallest that gives each CU a block and pads little.
+  auto padded = [&](long long block) { return (per + block - 1) / block * block; };
+  auto good = [&](long long block) { return rows / block >= 256 && 8 * padded(block) <= 9 * padded(32); };
   p.wq = good(128) ? 4 : good(64) ? 2 : 1;
   const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
   const long long most = 256 * per_cu(R, p.wq), units = blocks * (tiles > 0 ? tiles : 1);
   p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
+  p.start = 2 * blocks >= p.groups ? kStart / p.wq : 0;
   p.space = split_space(N, p.groups, 32 * p.wq, R);
   return p;
 }
@@ -115,7 +129,7 @@ struct Fp4 {
   static constexpr int kVal = kTile * R * 2, kBuffers = WQ == 1 ? 1 : 2;  // bytes of a tile's values, tiles of a group
   static constexpr int kQuery = WT * kBuffers * kVal, kQueries = far_at(KS + PS);
   static constexpr int kLds = kQuery + WQ * kQueries;
-  static constexpr int kPasses = 32 * R * 2 / (kQuery / 4);  // in which the queries go through a quarter of the values' LDS
+  static constexpr int kPasses = 32 * R * 2 / (kQuery / 4);  // the queries go through a quarter of the values' LDS
 };
 
 template <int R, int DR, int WQ>
@@ -143,7 +157,8 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
   const LaneAt<R> at(lane);
   const unsigned lds0 = lds_address(&lds[0]), val = lds0 + wt * (C::kBuffers * C::kVal);
   const unsigned query = lds0 + C::kQuery + wq * C::kQueries + lane * 16;  // the same for wavefronts of the same rows
-  // The lane's row of a tile in LDS, its part of piece p (16 E bytes of 32 E) at (put ^ 32 E p % 256) + 256 (32 E p / 256)
+  // The lane's row of a tile in LDS: its part of piece p (16 E bytes of 32 E) is at (put ^ 32 E p % 256) + 32 E p /
+  // 256 * 256.
   constexpr int E = C::E, kPieces = C::kPieces, kTurn = C::kTurn;
   const unsigned put = l32 * (R * 2) + ((E * half) ^ swizzle<R>(l32)) * 16;
 
@@ -152,11 +167,13 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
       base += sq.units();
       sq = sequence<C::kRows, kTile>(a, ++n);
     }
-    const int block = (int)((u - base) / sq.tiles), t0 = (int)((u - base) % sq.tiles);
-    const int t1 = (int)min((long long)sq.tiles, t0 + (end - u));
+    const int block = (int)((u - base) / sq.span), s0 = (int)((u - base) % sq.span);
+    const int s1 = (int)min((long long)sq.span, s0 + (end - u));
+    const int t0 = max(s0 - a.start, 0), t1 = s1 - a.start;
     const bool whole = t0 == 0 && t1 == sq.tiles;
     const int slot = 2 * group + (u == begin ? 0 : 1);
-    u += t1 - t0;
+    u += s1 - s0;
+    if (t1 <= t0) continue;  // only units in front of its tiles
     const int rows = sq.Lq * a.H, m0 = block * C::kRows;
     // the last cache row that a row of the block sees
     const int seen = sq.L - sq.Lq + (min(rows, m0 + C::kRows) - 1) / a.H;
@@ -178,7 +195,8 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
     if (turns > 0) {
       bf16x8 qf[KS + PS];
       // Through LDS (this wavefront's part of the values'), so that each load takes whole rows: 16 bytes a lane from 32
-      // rows would take 64 lines for a sixteenth of each.  A row that is not one reads the last again, and is not written.
+      // rows would take 64 lines for a part of each (18,000 cycles a block of 128 rows; 6,000).  A row that is not one
+      // reads the last again, and is not written.
       auto load_query = [&] {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what this wavefront put there last is there
         constexpr int kPasses = C::kPasses, kRun = kPieces / kPasses, kChunks = 2 * E * kRun, kAt = kChunks * 16;
@@ -222,7 +240,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
       int page = -1, off = 0;
       bool in = false, next_in = false;
       unsigned long long row = 0, row_end = 0;
-      auto look_up = [&](int i) {  // of tile i; compared without a sign: it may begin behind all rows that 31 bits count
+      auto look_up = [&](int i) {  // of tile i; compared without a sign: it may begin past what 31 bits count
         const int j = (t0 + wt + WT * i) * kTile + (lane_id() & 31);
         page = -1;
         if ((unsigned)j < (unsigned)last) {
@@ -246,7 +264,8 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
           *(u32x2*)(code + 2 * p) = *(global_u32x2*)from;
       };
       auto load_key = [&](int s) { pe[s] = *(global_u32x4*)((global_char*)row_end + 32 * s); };
-      // The scales in the order of the wavefront's pieces: R / 32 bytes, byte p (E = 2) or 2 p + half (E = 4) of piece p.
+      // The scales in the order of the wavefront's pieces: R / 32 bytes, piece p has byte p (E = 2) or 2 p + half (E =
+      // 4).
       constexpr int kBytes = E / 2, kRoll = kBytes * kTurn;
       auto load_scales = [&] {
         const auto from = (global_char*)row_end - 16 * (lane_id() >> 5) + 2 * DR;
@@ -275,8 +294,8 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
       };
       auto score = [&](u32x4 k, bf16x8 q, bool first) {
         if constexpr (R == 512) {
-          // In vector registers: the accumulators are full.  (The compiler takes all results of a kernel into one of the
-          // two halves of the register file.)  The waits that it would place are written out: 2 between a vector
+          // In vector registers: the accumulators are full.  (The compiler takes all results of a kernel into one of
+          // the two halves of the register file.)  The waits that it would place are written out: 2 between a vector
           // instruction's result and a matrix instruction that reads it.
           f32x16 x = S;
           if (first)
@@ -288,13 +307,16 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
           S = mma(__builtin_bit_cast(bf16x8, k), q, first ? f32x16{} : S);
         }
       };
-      // The scores of the tile in the registers (its values into `to`, the tile after it into the registers) and, where
-      // SUMS, beside them the sums of the tile in `from` with the weights P.  One wavefront issues an instruction every 4
-      // cycles at best (a conversion takes 8) and a product takes 32, so what is between two products is kept even.
+      // The scores of the tile in the registers (its values into `to`, the tile after it into the registers) and,
+      // where SUMS, beside them the sums of the tile in `from` with the weights P.  A wavefront issues an instruction
+      // every 4 cycles at best (a conversion takes 8) and a product takes 32, so what is between two products is kept
+      // even: 3,100 cycles a tile at R = 512, where the 68 products alone take 2,176 (4,200 in the order in which they
+      // were written).
       auto products = [&](auto scores_too, auto sums_too, unsigned from, unsigned to) {
         constexpr bool kScores = decltype(scores_too)::value, kSums = decltype(sums_too)::value;
-        // Steps that the reads of values are ahead.  With one buffer a tile is put where the one before is read: channels
-        // 64 p .. 64 p + 63 (32 p .. 32 p + 31) in steps E p .. E p + E - 1, so those of the E - 1 steps after have to be on their way.
+        // Steps that the reads of values are ahead.  With one buffer a tile is put where the one before is read: the
+        // 16 E channels of piece p in steps E p .. E p + E - 1, so those of the E - 1 steps after have to be on their
+        // way.
         constexpr int kFirst = C::kBuffers == 1 ? E : 2;
         static_assert(C::kBuffers > 1 || kFirst >= E);
         bf16x8 v[kFirst];
@@ -360,7 +382,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (kScores) {
           turn_scales();
-          // the waits between a matrix instruction's result and its use, which the compiler does not place for one written out
+          // the waits between a matrix instruction's result and its use, which the compiler does not place here
           if constexpr (R == 512) {
             f32x16 x = S;
             asm("s_nop 15\n\ts_nop 7" : "+v"(x));
@@ -477,7 +499,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
     m += (float)size;
     l = ldexpf(l, -size);
     float f[WT] = {1.f};
-    if constexpr (WT > 1) {  // one reference and sum for the wavefronts of the same rows; f: their factors, from this one on
+    if constexpr (WT > 1) {  // one reference and sum for the wavefronts of the same rows; f: their factors, from this one
       lds_barrier();  // all are done with the values
       if (id < 32) top[wave][row] = m, sums[wave][row] = l;
       lds_barrier();
@@ -580,7 +602,8 @@ hipError_t launch(const PagedWork& w, const Fp4Plan& p, hipStream_t stream) {
 template <int R, int DR>
 hipError_t launch(const PagedArgs& a, hipStream_t stream) {
   const Fp4Plan p = fp4_plan(a.N, a.Tq, a.H, R, DR, (long long)a.max_pages * a.page_size);
-  const PagedWork w = split_work(a, p.space);
+  PagedWork w = split_work(a, p.space);
+  w.a.start = p.start;
   switch (p.wq) {
     case 1: return launch<R, DR, 1>(w, p, stream);
     case 2: return launch<R, DR, 2>(w, p, stream);

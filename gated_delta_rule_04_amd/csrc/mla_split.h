@@ -2,8 +2,9 @@
 //
 // The rows of a sequence's queries (new token, head) are cut into blocks of ROWS,
 // the cache into tiles of TILE rows; a unit of work is a block and a tile.  Each
-// workgroup takes an equal, contiguous run of all units.  A block that ends up
-// split leaves float32 partial results (sums, running maximum and row sum) in its
+// workgroup takes an equal, contiguous run of all units, in front of each block
+// PagedArgs::start units that stand for what beginning it costs.  A block that
+// ends up split leaves float32 partial results (sums, running maximum and row sum) in its
 // workgroups' slots, which combine_kernel joins in order.
 #pragma once
 
@@ -23,8 +24,8 @@ struct PagedWork {
 
 // A sequence's share: its rows of q, its cache length and its units.
 struct Sequence {
-  int first, Lq, L, blocks, tiles;
-  __device__ __forceinline__ long long units() const { return (long long)blocks * tiles; }
+  int first, Lq, L, blocks, tiles, span;  // span: units of a block
+  __device__ __forceinline__ long long units() const { return (long long)blocks * span; }
 };
 template <int ROWS, int TILE>
 __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int n) {
@@ -36,6 +37,7 @@ __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int n) {
   s.L = min(max(a.lens[n], 0), a.max_pages * a.page_size);
   s.blocks = (s.Lq * a.H + ROWS - 1) / ROWS;
   s.tiles = max((s.L + TILE - 1) / TILE, 1);
+  s.span = a.start + s.tiles;
   return s;
 }
 
@@ -135,11 +137,11 @@ static __global__ __launch_bounds__(256) void combine_kernel(PagedWork w, int gr
   const long long in = row - (long long)s.first * a.H;
   if (in < 0 || in >= (long long)s.Lq * a.H) return;
   const long long share = (w.prefix[a.N] + groups - 1) / groups;
-  const long long u0 = w.prefix[n] + in / ROWS * s.tiles, u1 = u0 + s.tiles - 1;
-  const int g0 = (int)(u0 / share), g1 = (int)(u1 / share);
+  const long long u0 = w.prefix[n] + in / ROWS * s.span, u1 = u0 + s.span - 1;
+  const int g0 = (int)((u0 + a.start) / share), g1 = (int)(u1 / share);
   if (g0 == g1) return;  // in one piece: written already
   // part g's slot: its run's first segment, unless the block starts inside the run
-  auto place = [&](int g) { return (long long)(2 * g + (g == g0 && u0 != g0 * share ? 1 : 0)) * ROWS + in % ROWS; };
+  auto place = [&](int g) { return (long long)(2 * g + (g == g0 && u0 > g0 * share ? 1 : 0)) * ROWS + in % ROWS; };
   float m = -FLT_MAX;
   for (int g = g0 + (tid & 63); g <= g1; g += 64) m = fmaxf(m, w.ml[2 * place(g)]);
 #pragma unroll

@@ -33,7 +33,7 @@ __device__ __forceinline__ bf16x8 row_frag(const bf16* row, int s, int half) {
   return *(const bf16x8*)(row + 16 * s + 8 * half);
 }
 
-// Tiles in LDS: rows of W = 32 or 64 channels, or 128 and more, without padding (the
+// Tiles in LDS: rows of W = 64 channels or 128 and more, without padding (the
 // loads from global memory straight into LDS write 1024 bytes in a row), the
 // 16-byte pieces of each row permuted instead: piece p of row r lies at p ^
 // swizzle(r).  The LDS serves 16 lanes of a 16-byte read together, and 32 of a
@@ -41,9 +41,7 @@ __device__ __forceinline__ bf16x8 row_frag(const bf16* row, int s, int half) {
 // on 16 places of 256 bytes, and 4 consecutive rows' 64-byte runs on 4.
 template <int W>
 __device__ __forceinline__ constexpr int swizzle(int row) {
-  return W == 32   ? (row >> 2) & 3
-         : W == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3)
-                   : (row & 3) << 2 | ((row >> 2) & 3);
+  return W == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
 }
 
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;

@@ -127,7 +127,8 @@ def _append(name, fp4, c_kv, positions, slots, cache, latent_dim, rope, norm_wei
         H = q_pe.shape[1]
     dt, f32, i32 = c_kv.dtype, torch.float32, torch.int32
     dev = _check(c_kv, (cache, "cache", (cache.shape[0], cache.shape[1], row), torch.uint8 if fp4 else dt),
-                 (slots, "slots", (T,), i32), (positions, "positions", (T,), i32), (norm_weight, "norm_weight", (R,), f32),
+                 (slots, "slots", (T,), i32), (positions, "positions", (T,), i32),
+                 (norm_weight, "norm_weight", (R,), f32),
                  (rope, "rope", None if rope is None else (rope.shape[0], Dr), f32), (q_pe, "q_pe", (T, H, Dr), dt),
                  (q, "q", (T, H, D), dt))
     _call(name, dev, _ptr(c_kv), _ptr(norm_weight), float(eps), _ptr(rope),
@@ -199,8 +200,8 @@ def paged_attn(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=No
     cu_seqlens every sequence has one new token (q [N, H, R + Dr]); with it,
     sequence n's are rows cu[n] .. cu[n+1]-1 of q [Tq, H, R + Dr], the last of
     its seq_lens[n] cache rows.  Returns (o [Tq, H, R], lse [Tq, H])."""
-    return _paged("kda_mla_paged_attn", False, paged_workspace_bytes, q, cache, block_table, seq_lens, latent_dim, scale,
-                  cu_seqlens, out, lse, workspace)
+    return _paged("kda_mla_paged_attn", False, paged_workspace_bytes, q, cache, block_table, seq_lens, latent_dim,
+                  scale, cu_seqlens, out, lse, workspace)
 
 
 @functools.lru_cache(maxsize=256)
@@ -212,8 +213,8 @@ def paged_fp4_workspace_bytes(N, Tq, H, R, Dr, page_size, max_pages, dtype=torch
 def paged_attn_fp4(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens=None, out=None, lse=None,
                    workspace=None):
     """paged_attn over a 4-bit cache (cache_append_fp4), on the values that its rows stand for."""
-    return _paged("kda_mla_paged_attn_fp4", True, paged_fp4_workspace_bytes, q, cache, block_table, seq_lens, latent_dim,
-                  scale, cu_seqlens, out, lse, workspace)
+    return _paged("kda_mla_paged_attn_fp4", True, paged_fp4_workspace_bytes, q, cache, block_table, seq_lens,
+                  latent_dim, scale, cu_seqlens, out, lse, workspace)
 
 
 def cache_gather_fp4(cache, block_table, cu_seqlens, num_tokens, latent_dim, starts=None, out=None):
@@ -236,8 +237,8 @@ def cache_gather_fp4(cache, block_table, cu_seqlens, num_tokens, latent_dim, sta
                  (out, "out", (T, R + Dr), torch.bfloat16))
     if out is None:
         out = torch.empty((T, R + Dr), dtype=torch.bfloat16, device=dev)
-    _call("kda_mla_cache_gather_fp4", dev, _ptr(cache), _ptr(block_table), _ptr(cu_seqlens), _ptr(starts), _ptr(out), N, T,
-          R, Dr, num_pages, page_size, max_pages, KDA_BF16)
+    _call("kda_mla_cache_gather_fp4", dev, _ptr(cache), _ptr(block_table), _ptr(cu_seqlens), _ptr(starts), _ptr(out),
+          N, T, R, Dr, num_pages, page_size, max_pages, KDA_BF16)
     return out
 
 
@@ -264,7 +265,8 @@ def _outputs(out, sizes, workspace, need, dev):
     return {n: got[n] if n in got else out[n] for n in sizes}, workspace, nbytes
 
 
-def cache_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, num_tokens, out=None, workspace=None):
+def cache_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, num_tokens, out=None,
+               workspace=None):
     """Pages for a step's new tokens, from lengths on the GPU (all tensors int32): sequence n has seq_lens[n] rows in
     the cache and new_lens[n] new tokens; pages come from the end of the stack free_pages[:free_count] and are written
     into block_table [N, max_pages].  Sequences are served in order; one whose tokens do not fit its table's row or the
@@ -316,8 +318,8 @@ def cache_release(finished, seq_lens, block_table, free_pages, free_count, page_
                  *((t, "out[%r]" % n, (sizes[n],), i32) for n, t in (out or {}).items() if n in sizes))
     o, ws, nbytes = _outputs(out, sizes, workspace, _plan_bytes("release", N), dev)
     _call("kda_mla_cache_release", dev, _ptr(finished), _ptr(seq_lens), _ptr(block_table), _ptr(free_pages),
-          _ptr(free_count), free_pages.numel(), _ptr(o["seq_lens"]), _ptr(o["free_count"]), N, int(page_size), max_pages,
-          _ptr(ws), nbytes)
+          _ptr(free_count), free_pages.numel(), _ptr(o["seq_lens"]), _ptr(o["free_count"]), N, int(page_size),
+          max_pages, _ptr(ws), nbytes)
     return o
 
 
