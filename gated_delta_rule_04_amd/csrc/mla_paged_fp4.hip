@@ -140,7 +140,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
   __shared__ float top[4][32], sums[4][32];
   __shared__ int flags[4];
   const PagedArgs& a = w.a;
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wt = wave / WQ;
   Run run;
   Sequence sq;
@@ -154,13 +154,12 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
   int n = uniform((unsigned)run.n);
   sq = sequence<C::kRows, kTile>(a, n);
   const float c = a.scale * kda::kLog2e;
-  const LaneAt<R> at(lane);
   const unsigned lds0 = lds_address(&lds[0]), val = lds0 + wt * (C::kBuffers * C::kVal);
   const unsigned query = lds0 + C::kQuery + wq * C::kQueries + lane * 16;  // the same for wavefronts of the same rows
   // The lane's row of a tile in LDS: its part of piece p (16 E bytes of 32 E) is at (put ^ 32 E p % 256) + 32 E p /
   // 256 * 256.
   constexpr int E = C::E, kPieces = C::kPieces, kTurn = C::kTurn;
-  const unsigned put = l32 * (R * 2) + ((E * half) ^ swizzle<R>(l32)) * 16;
+  auto put = [](int id) { return (id & 31) * (R * 2) + ((E * (id >> 5)) ^ swizzle<R>(id & 31)) * 16; };
 
   for (long long u = begin; u < end;) {
     while (u >= base + sq.units()) {
@@ -182,7 +181,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
     const int turns = count <= 0 ? 0 : WQ == 1 ? (count - wt + WT - 1) / WT : (count + WT - 1) / WT;
     const int* table = a.table + (long long)n * a.max_pages;
     const int last = min(stop * kTile, sq.L);  // behind the last row of the run
-    const int mi = m0 + 32 * wq + l32;
+    const int mi = m0 + 32 * wq + (lane & 31);
     const bool on = mi < rows;
     const int lim = on ? sq.L - sq.Lq + mi / a.H : INT_MAX;  // the last cache row that the lane's row sees
     const bool idle = m0 + 32 * wq >= rows;  // no rows of its own: only its part of the values
@@ -246,7 +245,8 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         if ((unsigned)j < (unsigned)last) {
           const unsigned p = by_page.of(j);
           off = j - (int)p * a.page_size;
-          page = table[p];
+          // below 512 channels with a zero of its own: else it is one of a vector of zeros, which is spilled
+          page = R == 512 ? table[p] : table[(unsigned long long)opaque(0u) << 32 | p];
         }
       };
       auto find = [&] {  // the tile looked up last is the next
@@ -273,14 +273,32 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         for (int i = 0; i < C::kScales; ++i)
           next_scale[i] = *(global_u32*)(from + 4 * ((i + wq * kRoll / 4) % C::kScales));
       };
-      auto turn_scales = [&] {  // rows that are not there: 2^-127, any finite values
+      bool wide = false;               // a scale of 2^33 or more: bit 7 of a byte and one of the two below
+      unsigned bad = 0, next_bad = 0;  // the tile's rows with a scale that is NaN
+      // Rows that are not there have a scale of 2^-127, and so any finite values.  So have those with a NaN, whose scores
+      // are made NaN (mask): in the sums a value counts for rows that do not see it too, with a weight of 0.
+      auto turn_scales = [&] {
         const int h = E == 4 ? 8 * (lane_id() >> 5) : 0;
+        unsigned large = 0;
+#pragma unroll
+        for (int i = 0; i < C::kScales; ++i) large |= next_scale[i] & (next_scale[i] << 1 | next_scale[i] << 2);
+        next_bad = 0;
+        bool kept = next_in;
+        if (__any(kept && (large & 0x80808080u))) {
+          bool nan = false;
+#pragma unroll
+          for (int i = 0; i < C::kScales; ++i)
+            nan |= ((next_scale[i] & 0x7f7f7f7fu) + 0x01010101u & next_scale[i] & 0x80808080u) != 0;
+          next_bad = (unsigned)__ballot(kept && nan);
+          kept = kept && !nan;
+          wide |= kept && (large & 0x80808080u);
+        }
 #pragma unroll
         for (int i = 0; i < C::kScales; ++i) {
           const unsigned x = kRoll % 4 == 0 ? next_scale[i]
                                             : __builtin_amdgcn_alignbit(next_scale[(i + 1) % C::kScales], next_scale[i],
                                                                         wq * kRoll % 4 * 8);
-          scale[i] = next_in ? x >> h : 0u;
+          scale[i] = kept ? x >> h : 0u;
         }
       };
 
@@ -320,7 +338,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         constexpr int kFirst = C::kBuffers == 1 ? E : 2;
         static_assert(C::kBuffers > 1 || kFirst >= E);
         bf16x8 v[kFirst];
-        const unsigned at_from = opaque(from + at.col);
+        const unsigned at_from = opaque(from + LaneAt<R>(lane_id()).col);
         auto read = [&](int e) {  // A operand of step e: channels 32 (e / 2) .., rows 16 (e % 2) ..
           const int d = e / 2, to_tile = 16 * (e % 2) * (R * 2) + 256 * (d / 4);
           const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)((at_from ^ (64 * (d % 4))) + to_tile));
@@ -343,7 +361,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
           if (C::far(1)) far = far_query(1);
         }
         constexpr int kShare = 32 * E * kTurn;  // bytes of a row that this wavefront puts
-        const unsigned at_put = opaque(((to + put) ^ (wq * kShare % 256)) + 256 * (wq * kShare / 256));
+        const unsigned at_put = opaque(((to + put(lane_id())) ^ (wq * kShare % 256)) + 256 * (wq * kShare / 256));
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           u32x4 next = k;
@@ -391,7 +409,6 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         }
       };
       bool passed = false;  // a score is above its reference by more than 2^60
-      unsigned wide = 0;    // a scale of 2^33 or more: bit 7 of a byte and one of the two below
       auto highest = [&] {
         float x = S[0];
 #pragma unroll
@@ -401,8 +418,14 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
       auto mask = [&](int i) {
         const int j0 = (t0 + wt + WT * i) * kTile;
         const unsigned bits = (unsigned)__ballot(in);
-        if (bits == ~0u && j0 + kTile - 1 <= sq.L - sq.Lq + m0 / a.H) return;
+        if (bits == ~0u && bad == 0 && j0 + kTile - 1 <= sq.L - sq.Lq + m0 / a.H) return;
         const int h = 4 * (lane_id() >> 5), sees = lim - j0 - h;  // rows up to this one, of those from h on
+        if (bad != 0) {
+          const unsigned nans = bad >> h;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if ((nans >> acc_row(e, 0)) & 1) S[e] = __builtin_nanf("");
+        }
         const unsigned mine = bits >> h;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
@@ -417,8 +440,6 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
           sum += p[i];
         }
         l += sum;
-#pragma unroll
-        for (int i = 0; i < C::kScales; ++i) wide |= next_scale[i] & (next_scale[i] << 1 | next_scale[i] << 2);
         P[0] = acc_frag(p, 0);
         P[1] = acc_frag(p, 1);
         passed |= highest() > m + 60.f;
@@ -437,7 +458,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         load_scales();
       };
       auto step = [&](int i) {  // the tile in the registers becomes the present one, i
-        in = next_in;
+        in = next_in, bad = next_bad;
         find();
         look_up(i + 2);
       };
@@ -464,7 +485,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         if (WQ > 1) lds_barrier();
         products(no, yes, from, to);
         if (again) break;
-        again = __any(on && (passed || (wide & 0x80808080u)));
+        again = __any(on && (passed || wide));
         if (WQ > 1) {  // the wavefronts' loops have barriers: all do the run again, or none
           if (lane == 0) flags[wave] = again;
           lds_barrier();

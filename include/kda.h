@@ -659,7 +659,8 @@ kda_status kda_mla_cache_gather_fp4(const void* cache, const int* block_table, c
 /* kda_mla_paged_attn over a 4-bit cache, on the values that its rows stand for:
  * the same arguments, limits and errors, with cache [num_pages, page_size,
  * kda_mla_fp4_row_bytes(R, Dr)] bytes and a workspace of at least
- * kda_mla_paged_fp4_workspace_bytes(...) bytes. */
+ * kda_mla_paged_fp4_workspace_bytes(...) bytes.  Cache rows that a token does not
+ * see, those of later new tokens among them, may hold anything, NaN too. */
 size_t kda_mla_paged_fp4_workspace_bytes(int N, int Tq, int H, int R, int Dr, int page_size, int max_pages,
                                          kda_dtype dt);
 kda_status kda_mla_paged_attn_fp4(const void* q, const void* cache, const int* block_table, const int* seq_lens,

@@ -513,6 +513,34 @@ def test_paged_fp4_rows_of_other_sequences_do_not_matter(R, Dr, H):
     assert bool(torch.isnan(o2[1].float()).all())
 
 
+@pytest.mark.parametrize("height", [32, 64, 128])
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_rows_that_a_token_does_not_see_may_hold_nan(R, Dr, height):
+    """The cache rows of the last new tokens NaN (a scale, all scales, the rotary key): those tokens' outputs are NaN, the
+    others' bitwise what they were."""
+    H, N = 16, 4
+    q_lens = np.array([40, 7, 2, 33]) if height == 32 else _tokens(height, H, N, height + R)
+    q, cache, table, lens, cu = _paged(18, (q_lens + [70, 0, 31, 5]).tolist(), 16, H, R, Dr, q_lens=q_lens.tolist())
+    rows, _ = in_fp4(cache, R)
+    args = lambda: (*_cuda(q, rows, _i32(table), _i32(lens)), R, 0.07)  # noqa: E731
+    o, lse = mla.paged_attn_fp4(*args(), cu_seqlens=_i32(cu).cuda())
+    assert not bool(torch.isnan(o.float()).any())
+    keep = torch.ones(len(q), dtype=torch.bool, device="cuda")
+    for n, (first, what) in enumerate(((13, "scale"), (5, "scales"), (0, "key" if Dr else "scale"), (20, "scale"))):
+        for i in range(min(first, int(q_lens[n])), int(q_lens[n])):
+            j = int(lens[n]) - int(q_lens[n]) + i
+            row = rows[table[n][j // 16], j % 16]
+            at = R // 2 + 2 * Dr
+            if what == "key":
+                row[R // 2:at] = 255
+            else:
+                row[at + (i % (R // 32) if what == "scale" else 0):at + (i % (R // 32) + 1 if what == "scale" else R // 32)] = 255
+            keep[int(cu[n]) + i] = False
+    o2, lse2 = mla.paged_attn_fp4(*args(), cu_seqlens=_i32(cu).cuda())
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+    assert bool(torch.isnan(o2[~keep].float()).all()) and bool(torch.isnan(lse2[~keep]).all())
+
+
 def test_paged_fp4_many_sequences():
     """More sequences than threads of a workgroup: single tokens, and chunks with empty ones among them."""
     r = np.random.default_rng(23)
