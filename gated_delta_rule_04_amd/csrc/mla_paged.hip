@@ -335,7 +335,7 @@ template <int R, int DR, int WQ>
 hipError_t launch(const PagedWork& w, const PagedPlan& p, hipStream_t stream) {
   using C = Paged<R, DR, WQ>;
   paged_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w);
-  launch_combine<R, C::kRows, kTile>(w, p.groups, stream);
+  launch_combine<R, C::kRows, kTile>(w, p.groups, 8, stream);
   return hipGetLastError();
 }
 

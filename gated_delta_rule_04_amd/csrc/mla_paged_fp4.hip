@@ -24,6 +24,7 @@
 // found first; so a run takes three passes at most, and the loop has no rescaling
 // of the sums, which would cost them their place in the accumulators.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "mla_fp4.h"
@@ -71,8 +72,12 @@ Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   auto good = [&](long long block) { return rows / block >= 256 && 8 * padded(block) <= 9 * padded(32); };
   p.wq = good(128) ? 4 : good(64) ? 2 : 1;
   const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
-  const long long most = 256 * per_cu(R, p.wq), units = blocks * (tiles > 0 ? tiles : 1);
-  p.groups = (int)(units < most ? (units > 0 ? units : 1) : most);
+  // A tile for each wavefront, if there are too few for all workgroups, and so fewer parts to join (H96 R512 + 64, 2,000
+  // rows: 23.3 us with a workgroup a tile, 19.5 so; N8 H8 R256 of 1,000: 14.2 and 12.8; H12 R512 + 64, 900 rows: 16.4
+  // and 17.2).
+  const int at_once = 4 / p.wq;
+  const long long most = 256 * per_cu(R, p.wq), units = blocks * std::max((tiles + at_once - 1) / at_once, 1ll);
+  p.groups = (int)std::min(std::max(units, 1ll), most);
   p.start = 2 * blocks >= p.groups ? kStart / p.wq : 0;
   p.space = split_space(N, p.groups, 32 * p.wq, R);
   return p;
@@ -616,7 +621,10 @@ template <int R, int DR, int WQ>
 hipError_t launch(const PagedWork& w, const Fp4Plan& p, hipStream_t stream) {
   using C = Fp4<R, DR, WQ>;
   paged_fp4_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w, Divide(w.a.page_size));
-  launch_combine<R, C::kRows, kTile>(w, p.groups, stream);
+  // a block's parts: with few rows it pays sooner to join them by several workgroups a row (8 rows of 8 parts: the call
+  // 13.3 us with a wavefront a row, 10.3 with a workgroup for 64 channels)
+  const int few = (long long)w.a.Tq * w.a.H * (R / 64) <= 4096 ? 3 : 8;
+  launch_combine<R, C::kRows, kTile>(w, p.groups, few, stream);
   return hipGetLastError();
 }
 

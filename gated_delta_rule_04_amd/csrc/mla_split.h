@@ -183,13 +183,13 @@ static __global__ __launch_bounds__(256) void combine_kernel(PagedWork w, int gr
   if (a.lse && ch == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * (1.f / kda::kLog2e);
 }
 
+// `few`: parts a block can have up to which a row takes a wavefront, and with more several workgroups (8 rows of 15
+// parts: 4.2 us, with a wavefront a row 9.7 us; 6,144 rows of about 5 parts: 38 us, with a wavefront a row 13.5 us).
 template <int R, int ROWS, int TILE>
-void launch_combine(const PagedWork& w, int groups, hipStream_t stream) {
+void launch_combine(const PagedWork& w, int groups, int few, hipStream_t stream) {
   if (groups <= 1) return;
   const long long rows = (long long)w.a.Tq * w.a.H;
-  // Parts a block can have: with more than 8 a row takes several workgroups (8 rows of 15 parts: 4.2 us, with a
-  // wavefront a row 9.7 us; 6,144 rows of about 5 parts: 38 us, with a wavefront a row 13.5 us).
-  if (groups > 8 * (rows / ROWS + 1))
+  if (groups > few * (rows / ROWS + 1))
     combine_kernel<R, ROWS, TILE, true><<<dim3((unsigned)(rows * (R / 64))), dim3(256), 0, stream>>>(w, groups);
   else
     combine_kernel<R, ROWS, TILE, false><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream>>>(w, groups);
