@@ -53,36 +53,33 @@ struct Run {
 template <int ROWS, int TILE>
 __device__ __forceinline__ bool find_run(const PagedWork& w, int group, Run& run, Sequence& sq) {
   constexpr int kWaves = 4, kThreads = 64 * kWaves;
-  __shared__ long long scan[kWaves + 1];
+  __shared__ long long scan[kWaves];
   __shared__ long long found[2];
   const PagedArgs& a = w.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Inclusive sum over the workgroup of one value a thread; the total in scan[kWaves].
-  auto block_scan = [&](long long x) {
+  // Inclusive sum over the workgroup of one value a thread, and the total.
+  auto block_scan = [&](long long x, long long& all) {
     for (int m = 1; m < 64; m <<= 1) {
       const long long y = __shfl_up(x, m);
       if (lane >= m) x += y;
     }
-    __syncthreads();
+    if (a.N > kThreads) __syncthreads();  // the sums before are read
     if (lane == 63) scan[wave] = x;
     __syncthreads();
-    long long before = 0, all = 0;
+    all = 0;
     for (int i = 0; i < kWaves; ++i) {
-      if (i < wave) before += scan[i];
+      if (i < wave) x += scan[i];
       all += scan[i];
     }
-    __syncthreads();
-    if (tid == 0) scan[kWaves] = all;
-    __syncthreads();
-    return x + before;
+    return x;
   };
-  long long total = 0, mine = 0, incl = 0;
+  long long total = 0, mine = 0, incl = 0, all;
   for (int n0 = 0; n0 < a.N; n0 += kThreads) {
     const int n = n0 + tid;
     mine = n < a.N ? sequence<ROWS, TILE>(a, n).units() : 0;
-    incl = block_scan(mine) + total;
+    incl = block_scan(mine, all) + total;
     if (group == 0 && n < a.N) w.prefix[n] = incl - mine;
-    total += scan[kWaves];
+    total += all;
   }
   if (group == 0 && tid == 0) w.prefix[a.N] = total;
   const long long share = (total + gridDim.x - 1) / gridDim.x;
@@ -94,8 +91,8 @@ __device__ __forceinline__ bool find_run(const PagedWork& w, int group, Run& run
     if (a.N > kThreads) {
       const int n = n0 + tid;
       mine = n < a.N ? sequence<ROWS, TILE>(a, n).units() : 0;
-      incl = block_scan(mine) + before;
-      before += scan[kWaves];
+      incl = block_scan(mine, all) + before;
+      before += all;
     }
     if (incl - mine <= run.begin && run.begin < incl) {
       found[0] = n0 + tid;
