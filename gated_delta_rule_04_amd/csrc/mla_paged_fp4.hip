@@ -35,10 +35,9 @@ namespace {
 
 constexpr int kTile = 32;  // cache rows of a tile
 // Beginning a block (queries, first loads, handing the sums on) costs a workgroup as much as about 12 / WQ tiles.
-// Counted so where the work is cut, it keeps workgroups with the ends of short sequences from being the last (N64 H96
-// to 8,192 rows of 512 + 64: 118 us without, 111 with, N256 H8 to 2,048 rows of 256: 37 and 33; where all ends fall on
-// cuts, N256 H8 R256 of 2,048 each, it loses: 34 and 37).  Not where blocks are few and most workgroups have a part of
-// one.
+// Counted so where the work is cut, it keeps workgroups from having the ends of several short sequences (N64 H96 to
+// 8,192 rows of 512 + 64: 118 us without, 111 with, N256 H8 to 2,048 rows of 256: 37 and 33, N6 H64 to 274 rows of 512:
+// 31 and 23; where all ends fall on cuts, N256 H8 R256 of 2,048 each, it loses: 34 and 37).
 constexpr int kStart = 12;
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
@@ -78,7 +77,7 @@ Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   const int at_once = 4 / p.wq;
   const long long most = 256 * per_cu(R, p.wq), units = blocks * std::max((tiles + at_once - 1) / at_once, 1ll);
   p.groups = (int)std::min(std::max(units, 1ll), most);
-  p.start = 2 * blocks >= p.groups ? kStart / p.wq : 0;
+  p.start = blocks > 1 ? kStart / p.wq : 0;
   p.space = split_space(N, p.groups, 32 * p.wq, R);
   return p;
 }
