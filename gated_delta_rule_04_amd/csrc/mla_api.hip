@@ -199,7 +199,7 @@ kda_status kda_mla_cache_gather_fp4(const void* cache, const int* block_table, c
       (long long)num_pages * page_size > INT_MAX)
     return KDA_ERR_SHAPE;
   if (!latent_ok(R, Dr)) return KDA_ERR_UNSUPPORTED;
-  if ((long long)T * R > 1ll << 34) return KDA_ERR_SHAPE;  // 2048 channels a workgroup
+  if ((long long)T * R > 1ll << 34) return KDA_ERR_SHAPE;  // as documented; the grid has 32 rows a workgroup
   if (N == 0 || T == 0) return KDA_OK;
   if (!cu_seqlens || !rows || (num_pages > 0 && !cache) || (max_pages > 0 && !block_table)) return KDA_ERR_NULL;
   if (!aligned16(cache, rows)) return KDA_ERR_UNSUPPORTED;

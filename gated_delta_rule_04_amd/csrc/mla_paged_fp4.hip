@@ -119,7 +119,8 @@ struct Fp4 {
   static constexpr int E = R == 512 || (R == 256 && WQ > 1) ? 4 : 2, kPieces = KS / E, kScales = R / 128;
   static constexpr int kTurn = kPieces / WQ;  // the wavefronts of a tile begin so many pieces apart, and put the first
                                               // kTurn of their pieces into LDS for all
-  // At R = 512 there are no registers for all of the queries: the rotary part and those of some steps are in LDS.
+  // At R = 512, and with two workgroups a CU at R = 256, there are no registers for all of the queries: the rotary part
+  // and those of some steps are in LDS (each read of one takes the LDS as long as two of the values' reads).
   static constexpr bool far(int s) {
     if (R == 512) return s >= KS || s % 4 == 3 || (WQ != 2 && s % 8 == 1);
     if (R == 256) return WQ == 1 && (s >= KS || s % 2 == 1);

@@ -356,7 +356,7 @@ def _many(R, seed, hi=6000):
 @pytest.mark.parametrize("R,Dr", LATENT)
 @pytest.mark.parametrize("H,page", [(5, 16), (40, 64), (96, 100)])
 def test_paged_fp4_long_runs_of_tiles(R, Dr, H, page):
-    """Runs of many tiles a workgroup, over the ends of sequences, in each height of blocks."""
+    """Runs of many tiles a workgroup, over the ends of sequences."""
     print("CASE runs", R, Dr, H, page, flush=True)
     _check_all_rows("runs H%d R%d" % (H, R), *marked(H + R, _many(R, H), page, H, R, Dr, pool=9), R, 0.1)
 
