@@ -490,7 +490,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         if (WQ > 1) lds_barrier();
         products(no, yes, from, to);
         if (again) break;
-        again = __any(on && (passed || wide));
+        again = __any((on && passed) || wide);  // a lane's row of the block may not be there, its row of a tile counts
         if (WQ > 1) {  // the wavefronts' loops have barriers: all do the run again, or none
           if (lane == 0) flags[wave] = again;
           lds_barrier();

@@ -751,3 +751,50 @@ def test_two_fp4_calls_at_once_on_two_streams():
     for i, p in enumerate(got_p):
         for n in p:
             assert torch.equal(p[n], want_p[i % 2][n]), n
+
+
+# ---------------------------------------------------------------------------
+# large scales
+# ---------------------------------------------------------------------------
+def _far_above_with_a_large_block(seed, lens, H, R, Dr, q_lens=None, at=671, page=16):
+    """A cache row, the last of its tile, whose score is 2^48 above the others' and whose block of channels 64 .. 95, where
+    the queries are zero, is near 2^80: their product is past float32, the outputs are not.  Sequences share the pages."""
+    r = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    lens = np.asarray(lens, np.int32)
+    per = -(-int(lens.max()) // page)
+    order = r.permutation(per)
+    cu = None if q_lens is None else np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    q = 0.02 * torch.randn((len(lens) if cu is None else int(cu[-1]), H, R + Dr), generator=g)
+    q[..., 0], q[..., 64:96] = 1.0, 0.0
+    rows = torch.randn((per * page, R + Dr), generator=g)
+    rows[:, 0] = 0.0
+    rows[at, 0] = 48.0
+    rows[at, 64:96] *= 2.0 ** 80
+    cache = torch.empty((per, page, R + Dr))
+    cache[torch.as_tensor(order)] = rows.view(per, page, -1)
+    table = np.tile(order.astype(np.int32), (len(lens), 1))
+    return q.to(BF16), cache.to(BF16), table, lens, cu
+
+
+@pytest.mark.parametrize("H", [1, 5, 8, 31, 32, 40])
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_a_large_block_far_above_the_first_scores(R, Dr, H):
+    """Fewer rows than a block has (all of it: 32): the scales of all cache rows count, whichever lane has them."""
+    print("CASE large and far above", R, Dr, H, flush=True)
+    lens = np.random.default_rng(H).integers(900, 1100, 300)
+    _check_all_rows("large H%d R%d" % (H, R), *_far_above_with_a_large_block(151 + R + H, lens, H, R, Dr), R, float(np.log(2)))
+
+
+@pytest.mark.parametrize("height", [64, 128])
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_a_large_block_far_above_in_the_last_block(R, Dr, height):
+    """Taller blocks whose last one has fewer than 32 rows."""
+    print("CASE large and far above", R, Dr, height, flush=True)
+    H = 61
+    q_lens = _tokens(height, H, 9, height + R + Dr)
+    for n in (0, 5):
+        while not 0 < q_lens[n] * H % height < 31:
+            q_lens[n] += 1
+    args = _far_above_with_a_large_block(161 + R, q_lens + 900, H, R, Dr, q_lens=q_lens)
+    _check_all_rows("large, blocks of %d" % height, *args, R, float(np.log(2)))
