@@ -264,7 +264,8 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
 #pragma unroll
   for (int i = 0; i < kTimes; ++i) {
     const int r = i * kOnce + lane / kLanes;
-    const u32x4 v = fp4_values(codes[i], __builtin_bit_cast(float, scale[i] << 23));
+    const unsigned s = scale[i] >= kFp4NaN ? 255u : scale[i];
+    const u32x4 v = fp4_values(codes[i], __builtin_bit_cast(float, s << 23));
     if (r < count) *(u32x4*)(out + r * (R + DR) + 8 * c) = there[i] ? v : u32x4{};
   }
   if constexpr (DR > 0)

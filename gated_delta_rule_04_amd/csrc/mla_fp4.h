@@ -1,11 +1,14 @@
 // 4-bit latents (gfx950's v_cvt_scalef32 instructions: a code's value times the
 // power of two of a float32 scale, a scale byte shifted into its exponent; 255
-// gives NaN).
+// gives NaN).  A row's scale bytes from kFp4NaN on stand for NaN: their values
+// would leave bf16's range.
 #pragma once
 
 #include "mla_launch.h"
 
 namespace mla {
+
+constexpr unsigned kFp4NaN = 253;
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 

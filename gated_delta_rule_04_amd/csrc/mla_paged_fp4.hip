@@ -279,7 +279,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
           next_scale[i] = *(global_u32*)(from + 4 * ((i + wq * kRoll / 4) % C::kScales));
       };
       bool wide = false;               // a scale of 2^33 or more: bit 7 of a byte and one of the two below
-      unsigned bad = 0, next_bad = 0;  // the tile's rows with a scale that is NaN
+      unsigned bad = 0, next_bad = 0;  // the tile's rows with a scale that stands for NaN
       // Rows that are not there have a scale of 2^-127, and so any finite values.  So have those with a NaN, whose scores
       // are made NaN (mask): in the sums a value counts for rows that do not see it too, with a weight of 0.
       auto turn_scales = [&] {
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
           bool nan = false;
 #pragma unroll
           for (int i = 0; i < C::kScales; ++i)
-            nan |= ((next_scale[i] & 0x7f7f7f7fu) + 0x01010101u & next_scale[i] & 0x80808080u) != 0;
+            nan |= ((next_scale[i] & 0x7f7f7f7fu) + 0x01010101u * (256 - kFp4NaN) & next_scale[i] & 0x80808080u) != 0;
           next_bad = (unsigned)__ballot(kept && nan);
           kept = kept && !nan;
           wide |= kept && (large & 0x80808080u);

@@ -620,10 +620,12 @@ kda_status kda_mla_cache_release(const unsigned char* finished, const int* seq_l
  *                       2, 3, 4, 6 and their negatives
  *   [R/2, R/2 + 2 Dr)   the rotary key, bf16
  *   then R/32 bytes     E + 127 for channels 32b .. 32b+31, which are their codes'
- *                       values times 2^E; 255: all NaN
+ *                       values times 2^E; from 253 on (6 * 2^126 would pass
+ *                       bf16's range): all NaN
  *   then zeros up to a multiple of 16
  *
- * (codes and scales as MXFP4 of the OCP Microscaling Formats specification 1.0).
+ * (codes and scales as MXFP4 of the OCP Microscaling Formats specification 1.0, in
+ * which 253 and 254 are numbers).
  * A block's E is the smallest integer with max |c| <= 7 * 2^E, held to [-125, 125];
  * its channels divided by 2^E go to the nearest code value, ties to the even code,
  * above 6 to 6.  A block with a NaN or an infinity becomes NaN.  The values are
@@ -660,7 +662,8 @@ kda_status kda_mla_cache_gather_fp4(const void* cache, const int* block_table, c
  * the same arguments, limits and errors, with cache [num_pages, page_size,
  * kda_mla_fp4_row_bytes(R, Dr)] bytes and a workspace of at least
  * kda_mla_paged_fp4_workspace_bytes(...) bytes.  Cache rows that a token does not
- * see, those of later new tokens among them, may hold anything, NaN too. */
+ * see, those of later new tokens among them, may hold any bytes: NaN scales,
+ * scales that append does not write, infinite or NaN rotary keys. */
 size_t kda_mla_paged_fp4_workspace_bytes(int N, int Tq, int H, int R, int Dr, int page_size, int max_pages,
                                          kda_dtype dt);
 kda_status kda_mla_paged_attn_fp4(const void* q, const void* cache, const int* block_table, const int* seq_lens,

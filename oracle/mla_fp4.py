@@ -5,7 +5,9 @@ A latent block of 32 channels is held as 4-bit codes (sign, two bits of
 exponent, one of fraction: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one exponent E, the
 smallest with max|y| <= 7 * 2^E, held to [-125, 125] (MXFP4 of the OCP
 Microscaling Formats specification 1.0, which leaves the choice of E open).  A
-channel gets the nearest code, the even one of two equally near, and 6 above 6.
+scale byte (E + 127) from 253 on stands for NaN: 6 * 2^126 would pass bfloat16's
+range.  A channel gets the nearest code, the even one of two equally near, and 6
+above 6.
 """
 
 import numpy as np
@@ -39,7 +41,7 @@ def quantise(y):
 
 def values(codes, scales):
     """What codes [.., R] and scale bytes [.., R / 32] stand for."""
-    s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(int) - 127))
+    s = np.where(scales >= 253, np.nan, np.ldexp(1.0, scales.astype(int) - 127))
     return MAGNITUDES[codes & 7] * np.where(codes & 8, -1.0, 1.0) * np.repeat(s, 32, -1)
 
 

@@ -798,3 +798,65 @@ def test_paged_fp4_a_large_block_far_above_in_the_last_block(R, Dr, height):
             q_lens[n] += 1
     args = _far_above_with_a_large_block(161 + R, q_lens + 900, H, R, Dr, q_lens=q_lens)
     _check_all_rows("large, blocks of %d" % height, *args, R, float(np.log(2)))
+
+
+# ---------------------------------------------------------------------------
+# every scale byte
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_gather_of_every_scale(R, Dr):
+    r = np.random.default_rng(R + Dr)
+    page, n_pages, at = 16, 16, R // 2 + 2 * Dr
+    rows = np.zeros((n_pages * page, orc4.row_bytes(R, Dr)), np.uint8)
+    rows[:, :R // 2] = r.integers(0, 256, (len(rows), R // 2))
+    if Dr:
+        rows[:, R // 2:at] = _randn(R, len(rows), Dr).view(torch.uint8).numpy()
+    rows[:, at:at + R // 32] = (np.arange(len(rows))[:, None] + 64 * np.arange(R // 32)) % 256
+    want = orc4.unpack(rows, R, Dr)
+    assert np.isnan(want[:, :R]).sum() == 3 * R
+    table = np.arange(n_pages, dtype=np.int32)[None]
+    got = mla.cache_gather_fp4(*_cuda(torch.from_numpy(rows).view(n_pages, page, -1), _i32(table), _i32([0, len(rows)])),
+                               len(rows), R)
+    assert np.array_equal(got.cpu().double().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("scale", [253, 254])
+@pytest.mark.parametrize("height", [32, 64, 128])
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_rows_that_a_token_does_not_see_may_hold_scales_past_the_largest(R, Dr, height, scale):
+    """Cache rows of the last new tokens with a scale whose values bf16 does not have: NaN for those tokens, nothing for
+    the others."""
+    H, N, at = 16, 4, R // 2 + 2 * Dr
+    q_lens = np.array([40, 7, 2, 33]) if height == 32 else _tokens(height, H, N, height + R + 7)
+    q, cache, table, lens, cu = _paged(19, (q_lens + [70, 0, 31, 5]).tolist(), 16, H, R, Dr, q_lens=q_lens.tolist())
+    rows, _ = in_fp4(cache, R)
+    args = lambda: (*_cuda(q, rows, _i32(table), _i32(lens)), R, 0.07)  # noqa: E731
+    o, lse = mla.paged_attn_fp4(*args(), cu_seqlens=_i32(cu).cuda())
+    assert not bool(torch.isnan(o.float()).any())
+    keep = torch.ones(len(q), dtype=torch.bool, device="cuda")
+    for n, first in enumerate((13, 5, 1, 20)):
+        for i in range(min(first, int(q_lens[n])), int(q_lens[n])):
+            j = int(lens[n]) - int(q_lens[n]) + i
+            row, b = rows[table[n][j // 16], j % 16], i % (R // 32)
+            row[at + b] = scale
+            row[16 * b:16 * b + 16] = (0x77, 0x66, 0xee, 0xf7)[i % 4]  # 6 and 4, their negatives, both signs
+            keep[int(cu[n]) + i] = False
+    o2, lse2 = mla.paged_attn_fp4(*args(), cu_seqlens=_i32(cu).cuda())
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+    assert bool(torch.isnan(o2[~keep].float()).all()) and bool(torch.isnan(lse2[~keep]).all())
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_paged_fp4_smallest_and_largest_scales(R, Dr):
+    """Scale bytes 0, 1 and 252 in rows that every token sees; where the scale is the largest the queries are zero."""
+    q, cache, table, lens, cu = _paged(20, [150, 40], 16, 9, R, Dr)
+    q[..., 32:64] = 0
+    rows, _ = in_fp4(cache, R)
+    at = R // 2 + 2 * Dr
+    rows[:, :, at] = torch.arange(rows.shape[1]).to(torch.uint8) % 2
+    rows[table[0][5], 3, at + 1] = 252
+    vals = orc4.unpack(rows.numpy(), R, Dr)
+    o, lse = mla.paged_attn_fp4(*_cuda(q, rows, _i32(table), _i32(lens)), R, 0.07)
+    r = orc.paged_attention(q, vals, table, lens, R, 0.07)
+    _within("scales o", o, r[0], r[2])
+    _within("scales lse", lse, r[1], r[3])

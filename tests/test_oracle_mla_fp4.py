@@ -111,3 +111,10 @@ def test_plan_refuses_in_order():
     assert list(p["slots"][13:24]) == [24, 25, 26, 27, 20, 21, 22, 23, -1, 37, 38]
     p = orc.plan([3, 2], [0, 0], np.full((2, 3), -1), np.array([5, 6]), 2, 4, 4)  # the second's tokens end behind T
     assert p["kv_lens"] == [3, -1] and p["cu_seqlens"] == [0, 3, 4] and p["free_count"] == [1]
+
+
+def test_scales_past_the_largest_are_nan():
+    codes = np.tile(np.arange(16, dtype=np.uint8), (5, 2))
+    v = orc.values(codes, np.array([[0], [252], [253], [254], [255]], np.uint8))
+    assert np.isfinite(v[:2]).all() and v[0, 7] == 6 * 2.0 ** -127 and v[1, 15] == -6 * 2.0 ** 125
+    assert np.isnan(v[2:]).all()
