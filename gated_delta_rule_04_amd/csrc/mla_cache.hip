@@ -226,7 +226,8 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
   const int lane = threadIdx.x & 63, c = lane % kLanes;
   const long long t0 = ((long long)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)) * kGather;
   const int count = (int)(min(t0 + kGather, (long long)min(max(a.cu[a.N], 0), a.T)) - t0);
-  if (count <= 0) return;
+  const int skip = (int)min(max(min(max(a.cu[0], 0), a.T) - t0, 0ll), (long long)kGather);  // in front of the sequences
+  if (count <= skip) return;
   const int first = starts_before(a, t0), last = starts_before(a, t0 + count - 1);
   int place = -1;
   if (lane < count) {
@@ -266,10 +267,11 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
     const int r = i * kOnce + lane / kLanes;
     const unsigned s = scale[i] >= kFp4NaN ? 255u : scale[i];
     const u32x4 v = fp4_values(codes[i], __builtin_bit_cast(float, s << 23));
-    if (r < count) *(u32x4*)(out + r * (R + DR) + 8 * c) = there[i] ? v : u32x4{};
+    if (r >= skip && r < count) *(u32x4*)(out + r * (R + DR) + 8 * c) = there[i] ? v : u32x4{};
   }
   if constexpr (DR > 0)
-    if (pe_row < count) *(u32x4*)(out + pe_row * (R + DR) + R + 8 * (lane % 8)) = pe_place >= 0 ? pe : u32x4{};
+    if (pe_row >= skip && pe_row < count)
+      *(u32x4*)(out + pe_row * (R + DR) + R + 8 * (lane % 8)) = pe_place >= 0 ? pe : u32x4{};
 }
 
 template <int R, int DR>

@@ -219,8 +219,8 @@ def paged_attn_fp4(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlen
 
 def cache_gather_fp4(cache, block_table, cu_seqlens, num_tokens, latent_dim, starts=None, out=None):
     """Rows of a 4-bit cache as bfloat16 [num_tokens, R + Dr], sequence after sequence: row cu_seqlens[n] + i is row
-    starts[n] + i (None: i) of sequence n; one that is not in the cache is zeros.  Rows behind the last sequence are
-    left as they were.  Dr follows from the cache's row bytes."""
+    starts[n] + i (None: i) of sequence n; one that is not in the cache is zeros.  Rows in front of the first sequence
+    and behind the last are left as they were.  Dr follows from the cache's row bytes."""
     if cache.dim() != 3 or block_table.dim() != 2:
         raise ValueError("cache must be [num_pages, page_size, row], block_table [N, max_pages]")
     num_pages, page_size, row = cache.shape

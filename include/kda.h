@@ -646,11 +646,11 @@ kda_status kda_mla_cache_append_fp4(const void* c_kv, const float* norm_weight, 
  *
  *   rows   [T, R + Dr] dt: row cu_seqlens[n] + i is row starts[n] + i of sequence
  *          n.  One that is not in the cache (before 0 or behind max_pages *
- *          page_size, or of a page outside [0, num_pages)) is zeros.  Rows from
- *          cu_seqlens[N] on are left as they were.
+ *          page_size, or of a page outside [0, num_pages)) is zeros.  Rows in
+ *          front of cu_seqlens[0] and from cu_seqlens[N] on are left as they were.
  *   cache, block_table  as for kda_mla_paged_attn_fp4
- *   cu_seqlens  device int32 [N + 1], clamped into [0, T];  starts device int32
- *          [N] or NULL (0)
+ *   cu_seqlens  device int32 [N + 1], non-decreasing, clamped into [0, T];
+ *          starts  device int32 [N] or NULL (0)
  * Sizes as for kda_mla_paged_attn, T at most 2^27, T * R at most 2^34.  N = 0 or
  * T = 0 is a no-op.
  */

@@ -860,3 +860,16 @@ def test_paged_fp4_smallest_and_largest_scales(R, Dr):
     r = orc.paged_attention(q, vals, table, lens, R, 0.07)
     _within("scales o", o, r[0], r[2])
     _within("scales lse", lse, r[1], r[3])
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+def test_gather_leaves_rows_in_front_of_the_first_sequence(R, Dr):
+    rows, vals = in_fp4(_randn(R + 1, 9, 24, R + Dr), R)
+    table = np.random.default_rng(R).integers(0, 9, (3, 4)).astype(np.int32)
+    for first in (1, 7, 8, 13, 40):
+        cu = np.array([first, first + 3, first + 3, first + 30], np.int32)
+        starts = np.array([50, 2, 9], np.int32)
+        T = first + 35
+        out = torch.full((T, R + Dr), CANARY, dtype=BF16, device="cuda")
+        mla.cache_gather_fp4(*_cuda(rows, _i32(table), _i32(cu)), T, R, starts=_i32(starts).cuda(), out=out)
+        assert np.array_equal(out.cpu().double().numpy(), _gather_want(vals, table, cu, starts, T)), first
