@@ -87,11 +87,11 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wd = wave / WQ;
 
   Run run;
-  Sequence sq;
-  if (!find_run<C::kRows, kTile>(w, blockIdx.x, run, sq)) return;
+  if (!find_run<C::kRows, kTile>(w, blockIdx.x, run)) return;
   const long long begin = run.begin, end = run.end;
-  int n = run.n;
   long long base = run.base;  // units before sequence n
+  int n = run.n;
+  Sequence sq = sequence<C::kRows, kTile>(a, n);
   const float c = a.scale * kda::kLog2e;
   const unsigned lds_lat = lds_address(&lat[0][0]), lds_rot = lds_address(&rot[0][0]);
   const LaneAt<R> at_lat(lane);

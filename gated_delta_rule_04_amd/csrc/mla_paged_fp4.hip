@@ -148,16 +148,14 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wq = wave % WQ, wt = wave / WQ;
   Run run;
-  Sequence sq;
   // Workgroups go round the 8 XCDs: neighbours in the work, which share queries or cache rows, are put on one.
   const int xcd = blockIdx.x % 8, each = gridDim.x / 8, over = gridDim.x % 8;
   const int group = xcd * each + min(xcd, over) + blockIdx.x / 8;
-  if (!find_run<C::kRows, kTile>(w, group, run, sq)) return;
-  // The same in all lanes, and said so: what follows from them stays in scalar registers.
-  const long long begin = uniform((unsigned long long)run.begin), end = uniform((unsigned long long)run.end);
-  long long base = uniform((unsigned long long)run.base);  // units before sequence n
-  int n = uniform((unsigned)run.n);
-  sq = sequence<C::kRows, kTile>(a, n);
+  if (!find_run<C::kRows, kTile>(w, group, run)) return;
+  const long long begin = run.begin, end = run.end;
+  long long base = run.base;  // units before sequence n
+  int n = run.n;
+  Sequence sq = sequence<C::kRows, kTile>(a, n);
   const float c = a.scale * kda::kLog2e;
   const unsigned lds0 = lds_address(&lds[0]), val = lds0 + wt * (C::kBuffers * C::kVal);
   const unsigned query = lds0 + C::kQuery + wq * C::kQueries + lane * 16;  // the same for wavefronts of the same rows
