@@ -153,8 +153,7 @@ static kda_status paged_attn(bool fp4, const void* q, const void* cache, const i
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return KDA_ERR_WORKSPACE;
   mla::PagedArgs a;
   a.q = static_cast<const mla::bf16*>(q);
-  a.cache = static_cast<const mla::bf16*>(cache);
-  a.cache4 = static_cast<const unsigned char*>(cache);
+  a.cache = cache;
   a.table = block_table;
   a.lens = seq_lens;
   a.cu = cu_seqlens;

@@ -65,8 +65,7 @@ hipError_t launch_release(const ReleaseArgs& p, hipStream_t stream);
 
 struct PagedArgs {
   const bf16* q;      // [Tq][H][R + Dr]
-  const bf16* cache;  // [num_pages * page_size][R + Dr]
-  const unsigned char* cache4;  // or [num_pages * page_size][fp4_row_bytes]
+  const void* cache;  // [num_pages * page_size] rows: bf16 [R + Dr], or fp4_row_bytes(R, Dr) bytes
   const int* table;   // [N][max_pages]
   const int* lens;    // [N]
   const int* cu;      // [N + 1] or NULL: one token a sequence
@@ -74,8 +73,8 @@ struct PagedArgs {
   float* lse;         // [Tq][H] or NULL
   int N, Tq, H, num_pages, page_size, max_pages;
   float scale;
-  void* ws;
   int start = 0;  // what beginning a block of rows costs, in tiles, where the work is cut evenly
+  void* ws;
 };
 size_t paged_workspace(int N, int Tq, int H, int R, int Dr, long long max_len);
 hipError_t launch_paged(int R, int Dr, const PagedArgs& a, hipStream_t stream);

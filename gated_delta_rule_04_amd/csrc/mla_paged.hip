@@ -92,6 +92,7 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
   long long base = run.base;  // units before sequence n
   int n = run.n;
   Sequence sq = sequence<C::kRows, kTile>(a, n);
+  const bf16* const cache = static_cast<const bf16*>(a.cache);
   const float c = a.scale * kda::kLog2e;
   const unsigned lds_lat = lds_address(&lat[0][0]), lds_rot = lds_address(&rot[0][0]);
   const LaneAt<R> at_lat(lane);
@@ -138,13 +139,13 @@ __global__ __launch_bounds__((Paged<R, DR, WQ>::kThreads), 1) void paged_kernel(
       const int r0 = (wave + C::kWaves * i) * kPer, r = r0 + lane / (R / 8);
       const unsigned to = lds_lat + (b * kTile + r0) * (R * 2);
       if constexpr (R == 512)  // a row a load: its address is scalar
-        load_lds_if(on, a.cache + (long long)__builtin_amdgcn_readlane(from, r0) * D, (lane ^ swizzle<R>(r0)) * 16, to);
+        load_lds_if(on, cache + (long long)__builtin_amdgcn_readlane(from, r0) * D, (lane ^ swizzle<R>(r0)) * 16, to);
       else
-        load_lds_if(on, a.cache + (long long)__shfl(from, r) * D + ((lane % (R / 8)) ^ swizzle<R>(r)) * 8, to);
+        load_lds_if(on, cache + (long long)__shfl(from, r) * D + ((lane % (R / 8)) ^ swizzle<R>(r)) * 8, to);
     };
     auto fetch_rot = [&](int i, int from, int b, unsigned long long on) {
       const int r0 = (wave + C::kWaves * i) * 8, r = r0 + lane / 8;
-      load_lds_if(on, a.cache + (long long)__shfl(from, r) * D + R + ((lane % 8) ^ swizzle<64>(r)) * 8,
+      load_lds_if(on, cache + (long long)__shfl(from, r) * D + R + ((lane % 8) ^ swizzle<64>(r)) * 8,
                   lds_rot + (b * kTile + r0) * (DR * 2));
     };
 

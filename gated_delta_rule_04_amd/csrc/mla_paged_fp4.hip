@@ -256,8 +256,8 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
         next_in = (unsigned)page < (unsigned)a.num_pages;
         const long long r = next_in ? page * a.page_size + off : 0;
         const int h = lane_id() >> 5;
-        row = (unsigned long long)a.cache4 + r * kRow + 4 * E * h;
-        row_end = (unsigned long long)a.cache4 + r * kRow + R / 2 + 16 * h;
+        row = (unsigned long long)a.cache + r * kRow + 4 * E * h;
+        row_end = (unsigned long long)a.cache + r * kRow + R / 2 + 16 * h;
       };
       auto load_codes = [&](int p) {
         const auto from = (global_char*)row + 8 * E * ((p + wq * kTurn) % kPieces);

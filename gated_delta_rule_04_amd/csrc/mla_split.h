@@ -21,6 +21,9 @@ struct PagedWork {
   float* ml;          // [2 * groups][block rows][2]
   float* po;          // [2 * groups][block rows][R]
 };
+// A kernel's arguments, these and 8 bytes more, are in two lines of 64 bytes: with a third one to fetch, the join and the
+// 4-bit cache's kernels take 0.2 to 0.4 us longer (the join of one sequence of 131,072 rows 5.8 and 6.2 us).
+static_assert(sizeof(PagedWork) + 8 <= 128, "two lines");
 
 // A sequence's share: its rows of q, its cache length and its units.
 struct Sequence {
