@@ -48,7 +48,10 @@ SOURCE_FLAGS = {
     # file: without it the paged attention's 256 registers of sums at 512
     # channels spill (513 registers; 14 with it), and dk, dv at 128 + 64
     # channels take 380 registers, not 339.
-    "mla_paged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    # Its loops begin at a line of 64 bytes: where they happen to lie otherwise
+    # moves with any change in front of them, and costs up to 1.5% (N256 H8 R256
+    # to 2,048: 45.6 to 45.8 us, 45.1 so).
+    "mla_paged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1", "-falign-loops=64"],
     "mla_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
