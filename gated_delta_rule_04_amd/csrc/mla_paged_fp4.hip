@@ -187,7 +187,6 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
     const int mi = m0 + 32 * wq + (lane & 31);
     const bool on = mi < rows;
     const int lim = on ? sq.L - sq.Lq + mi / a.H : INT_MAX;  // the last cache row that the lane's row sees
-    const bool idle = m0 + 32 * wq >= rows;  // no rows of its own: only its part of the values
 
     f32x16 acc[kOut];
 #pragma unroll
