@@ -873,3 +873,17 @@ def test_gather_leaves_rows_in_front_of_the_first_sequence(R, Dr):
         out = torch.full((T, R + Dr), CANARY, dtype=BF16, device="cuda")
         mla.cache_gather_fp4(*_cuda(rows, _i32(table), _i32(cu)), T, R, starts=_i32(starts).cuda(), out=out)
         assert np.array_equal(out.cpu().double().numpy(), _gather_want(vals, table, cu, starts, T)), first
+
+
+@pytest.mark.parametrize("R,Dr", LATENT)
+@pytest.mark.parametrize("height,H", [(64, 16), (128, 64)])
+def test_paged_fp4_many_sequences_in_blocks_of_more_rows(R, Dr, height, H):
+    """More sequences than threads of a workgroup, four tokens each on average, empty ones and short caches among them."""
+    print("CASE many, blocks", R, Dr, height, flush=True)
+    N, r = 300, np.random.default_rng(R + height)
+    q_lens = r.integers(0, 9, N)
+    q_lens[N // 2:] = 8 - q_lens[:N // 2]
+    assert 4 * N * H // height >= 256 and (height == 128 or 4 * N * H // 128 < 256)
+    lens = np.maximum(r.integers(0, 300, N), q_lens)
+    lens[7::50] = q_lens[7::50] // 2  # rows that see nothing
+    _check_all_rows("many R%d" % R, *marked(171 + R, lens, 16, H, R, Dr, q_lens=q_lens, pool=9), R, 0.1)
