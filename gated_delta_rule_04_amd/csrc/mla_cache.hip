@@ -226,10 +226,10 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
   const int lane = threadIdx.x & 63, c = lane % kLanes;
   const long long t0 = ((long long)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)) * kGather;
   const int count = (int)(min(t0 + kGather, (long long)min(max(a.cu[a.N], 0), a.T)) - t0);
-  const int skip = (int)min(max(min(max(a.cu[0], 0), a.T) - t0, 0ll), (long long)kGather);  // in front of the sequences
-  if (count <= skip) return;
+  if (count <= 0) return;
   const int first = starts_before(a, t0), last = starts_before(a, t0 + count - 1);
-  int place = -1;
+  constexpr int kMissing = -1, kLeave = -2;  // no cache row; no row of a sequence: left as it was
+  int place = kLeave;
   if (lane < count) {
     const long long t = t0 + lane;
     int lo = first, hi = last + 1;
@@ -240,8 +240,9 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
       else
         hi = mid;
     }
-    const long long j = t - min(max(a.cu[lo], 0), a.T) + (a.starts ? a.starts[lo] : 0);
-    if (j >= 0 && j < (long long)a.max_pages * a.page_size) {
+    const long long in = t - min(max(a.cu[lo], 0), a.T), j = in + (a.starts ? a.starts[lo] : 0);
+    if (in >= 0) place = kMissing;
+    if (in >= 0 && j >= 0 && j < (long long)a.max_pages * a.page_size) {
       const unsigned p = (unsigned)j / (unsigned)a.page_size;
       const int page = a.table[(long long)lo * a.max_pages + p];
       if ((unsigned)page < (unsigned)a.num_pages) place = page * a.page_size + (int)((unsigned)j - p * a.page_size);
@@ -253,13 +254,12 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
   u32x4 pe = {};
   if constexpr (DR > 0) pe = *(global_u32x4*)(row(pe_place) + R / 2 + 16 * (lane % 8));
   unsigned codes[kTimes], scale[kTimes];
-  bool there[kTimes];
+  int at[kTimes];
 #pragma unroll
   for (int i = 0; i < kTimes; ++i) {
-    const int at = __shfl(place, i * kOnce + lane / kLanes);
-    there[i] = at >= 0;
-    codes[i] = *(global_u32*)(row(at) + 4 * c);
-    scale[i] = *(global_u8*)(row(at) + R / 2 + 2 * DR + c / 4);
+    at[i] = __shfl(place, i * kOnce + lane / kLanes);
+    codes[i] = *(global_u32*)(row(at[i]) + 4 * c);
+    scale[i] = *(global_u8*)(row(at[i]) + R / 2 + 2 * DR + c / 4);
   }
   bf16* const out = a.rows + t0 * (R + DR);
 #pragma unroll
@@ -267,10 +267,10 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a) {
     const int r = i * kOnce + lane / kLanes;
     const unsigned s = scale[i] >= kFp4NaN ? 255u : scale[i];
     const u32x4 v = fp4_values(codes[i], __builtin_bit_cast(float, s << 23));
-    if (r >= skip && r < count) *(u32x4*)(out + r * (R + DR) + 8 * c) = there[i] ? v : u32x4{};
+    if (at[i] != kLeave) *(u32x4*)(out + r * (R + DR) + 8 * c) = at[i] >= 0 ? v : u32x4{};
   }
   if constexpr (DR > 0)
-    if (pe_row >= skip && pe_row < count)
+    if (pe_place != kLeave)
       *(u32x4*)(out + pe_row * (R + DR) + R + 8 * (lane % 8)) = pe_place >= 0 ? pe : u32x4{};
 }
 
