@@ -34,10 +34,11 @@ namespace mla {
 namespace {
 
 constexpr int kTile = 32;  // cache rows of a tile
-// Beginning a block (queries, first loads, handing the sums on) costs a workgroup as much as about 12 / WQ tiles.
-// Counted so where the work is cut, it keeps workgroups from having the ends of several short sequences (N64 H96 to
-// 8,192 rows of 512 + 64: 118 us without, 111 with, N256 H8 to 2,048 rows of 256: 37 and 33, N6 H64 to 274 rows of 512:
-// 31 and 23; where all ends fall on cuts, N256 H8 R256 of 2,048 each, it loses: 34 and 37).
+// What beginning and ending a block costs (queries, first loads, handing the sums on), counted as 12 / WQ tiles of a
+// workgroup where the work is cut: it keeps workgroups from having the ends of several short sequences (N64 H96 to
+// 8,192 rows of 512 + 64: 124 us without, 117 with, N256 H8 to 2,048 rows of 256: 34 and 31, N6 H64 to 274 rows of 512:
+// 30 and 23, N31 H96 to 1,781 rows of 256 + 64: 37 and 30; where all ends fall on cuts, N256 H8 R256 of 2,048 each, it
+// loses: 32 and 35).  At R = 512 it is 31,000 cycles of a wavefront in fact, and a tile 4,350.
 constexpr int kStart = 12;
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
@@ -56,24 +57,26 @@ struct Fp4Plan {
 };
 
 // Workgroups that a CU holds (a wavefront a SIMD each), by their registers.  256 channels: in blocks of 32 rows two
-// with pieces of two steps fill each other's waits in short runs (N256 H8 to 2,048: 35 us, one with pieces of four 44;
-// in long ones, of 8,192, 116 and 104); in taller blocks one with all queries in registers (N256 H128 of 8,192: 305
-// us, two 381).
+// with pieces of two steps fill each other's waits in short ragged runs (N256 H8 to 2,048: 31.5 us, one with pieces of
+// four and all queries in registers 33.0), and lose in even and long ones (2,048 each 34.5 and 30.1 us, 8,192 each 114
+// and 95), most with a rotary part, where the two have 32 registers spilled and each reload in the tile loop waits for
+// the tile on its way (N256 H8 R256 + 64 of 2,048: 79 and 45 us).  In taller blocks one.
 constexpr int per_cu(int R, int wq) { return R == 512 || (R == 256 && wq > 1) ? 1 : 2; }
 
 Fp4Plan fp4_plan(int N, int Tq, int H, int R, int Dr, long long max_len) {
   Fp4Plan p;
   const long long rows = (long long)Tq * H, per = N ? (rows + N - 1) / N : 0;
   // Taller blocks convert and put a tile for fewer rows each and read the cache less often (4 chunks of 512 tokens, 96
-  // heads of 512 + 64: 1.98 ms with 128 rows, 2.1 with 64, 2.4 with 32); lower ones cut evenly and pad less (N64 H96 to
-  // 8,192: 122 us with 32 rows, 137 with 64, 139 with 128).  So the tallest that gives each CU a block and pads little.
+  // heads of 512 + 64: 1.97 ms with 128 rows, 2.04 with 64, 2.22 with 32); lower ones cut evenly and pad less (N64 H96
+  // to 8,192: 117 us with 32 rows, 121 with 64, 123 with 128; of 16,384 each, past the last-level cache, 368 with 32
+  // and 309 with 128).  So the tallest that gives each CU a block and pads little.
   auto padded = [&](long long block) { return (per + block - 1) / block * block; };
   auto good = [&](long long block) { return rows / block >= 256 && 8 * padded(block) <= 9 * padded(32); };
   p.wq = good(128) ? 4 : good(64) ? 2 : 1;
   const long long blocks = rows / (32 * p.wq) + N, tiles = (max_len + kTile - 1) / kTile;
-  // A tile for each wavefront, if there are too few for all workgroups, and so fewer parts to join (H96 R512 + 64, 2,000
-  // rows: 23.3 us with a workgroup a tile, 19.5 so; N8 H8 R256 of 1,000: 14.2 and 12.8; H12 R512 + 64, 900 rows: 16.4
-  // and 17.2).
+  // A tile for each wavefront, if there are too few for all workgroups, and so fewer parts to join (H96 R512 + 64,
+  // 2,000 rows: 23.5 us with a workgroup a tile, 20.0 so; N8 H8 R256 of 1,000: no difference; H12 R512 + 64, 900 rows:
+  // 16.8 and 17.3).
   const int at_once = 4 / p.wq;
   const long long most = 256 * per_cu(R, p.wq), units = blocks * std::max((tiles + at_once - 1) / at_once, 1ll);
   p.groups = (int)std::min(std::max(units, 1ll), most);
@@ -120,7 +123,8 @@ struct Fp4 {
   static constexpr int kTurn = kPieces / WQ;  // the wavefronts of a tile begin so many pieces apart, and put the first
                                               // kTurn of their pieces into LDS for all
   // At R = 512, and with two workgroups a CU at R = 256, there are no registers for all of the queries: the rotary part
-  // and those of some steps are in LDS (each read of one takes the LDS as long as two of the values' reads).
+  // and those of some steps are in LDS (each read of one takes the LDS as long as two of the values' reads).  At 256 +
+  // 64 with two, that does not suffice (per_cu).
   static constexpr bool far(int s) {
     if (R == 512) return s >= KS || s % 4 == 3 || (WQ != 2 && s % 8 == 1);
     if (R == 256) return WQ == 1 && (s >= KS || s % 2 == 1);
@@ -330,8 +334,7 @@ __global__ __launch_bounds__(256, per_cu(R, WQ)) void paged_fp4_kernel(PagedWork
       // The scores of the tile in the registers (its values into `to`, the tile after it into the registers) and,
       // where SUMS, beside them the sums of the tile in `from` with the weights P.  A wavefront issues an instruction
       // every 4 cycles at best (a conversion takes 8) and a product takes 32, so what is between two products is kept
-      // even: 3,100 cycles a tile at R = 512, where the 68 products alone take 2,176 (4,200 in the order in which they
-      // were written).
+      // even: 3,700 cycles a tile at R = 512, where the 68 products alone take 2,176.
       auto products = [&](auto scores_too, auto sums_too, unsigned from, unsigned to) {
         constexpr bool kScores = decltype(scores_too)::value, kSums = decltype(sums_too)::value;
         // Steps that the reads of values are ahead.  With one buffer a tile is put where the one before is read: the
@@ -618,8 +621,8 @@ template <int R, int DR, int WQ>
 hipError_t launch(const PagedWork& w, const Fp4Plan& p, hipStream_t stream) {
   using C = Fp4<R, DR, WQ>;
   paged_fp4_kernel<R, DR, WQ><<<dim3(p.groups), dim3(C::kThreads), 0, stream>>>(w, Divide(w.a.page_size));
-  // a block's parts: with few rows it pays sooner to join them by several workgroups a row (8 rows of 8 parts: the call
-  // 13.3 us with a wavefront a row, 10.3 with a workgroup for 64 channels)
+  // a block's parts: with few rows it pays sooner to join them by several workgroups a row (8 rows of 8 parts: 6.0 us
+  // with a wavefront a row, 3.9 with a workgroup for 64 channels)
   const int few = (long long)w.a.Tq * w.a.H * (R / 64) <= 4096 ? 3 : 8;
   launch_combine<R, C::kRows, kTile>(w, p.groups, few, stream);
   return hipGetLastError();

@@ -21,8 +21,8 @@ struct PagedWork {
   float* ml;          // [2 * groups][block rows][2]
   float* po;          // [2 * groups][block rows][R]
 };
-// A kernel's arguments, these and 8 bytes more, are in two lines of 64 bytes: with a third one to fetch, the join and the
-// 4-bit cache's kernels take 0.2 to 0.4 us longer (the join of one sequence of 131,072 rows 5.8 and 6.2 us).
+// A kernel's arguments, these and 8 bytes more, are in two lines of 64 bytes: with a third one to fetch, the join and
+// the 4-bit cache's kernels take 0.2 to 0.4 us longer (the join of one sequence of 131,072 rows 5.8 and 6.2 us).
 static_assert(sizeof(PagedWork) + 8 <= 128, "two lines");
 
 // A sequence's share: its rows of q, its cache length and its units.
@@ -53,7 +53,8 @@ struct Run {
 
 // Finds the run of workgroup `group` (256 threads); false when there is none.  Workgroup 0 writes the sequences' prefix
 // for the join.  A run is the same in all lanes, and said so: what follows from it stays in scalar registers (the bf16
-// cache, R 512 + 64 in blocks of 128 rows: 14 vector registers spilled, 18 if not said; N64 H96 to 8,192 155 us and 164).
+// cache, R 512 + 64 in blocks of 128 rows: 14 vector registers spilled, 18 if not said; N64 H96 to 8,192: 155 us and
+// 164).
 template <int ROWS, int TILE>
 __device__ __forceinline__ bool find_run(const PagedWork& w, int group, Run& run) {
   constexpr int kWaves = 4, kThreads = 64 * kWaves;
